@@ -13,6 +13,9 @@ PyTorch fallback, and a missing or unloadable library raises.
   act_quant_store(x, slot_mapping, k_pages, s_pages)     bf16 keys -> fp8 key pool
   prepare_ragged(seq_len, q_len, req_idx, req_to_token, q_cap)  ragged ks/ke (+ index copy)
   topk_transform(idx, page_table, page_size, ...)        selected positions -> physical slots
+  latent_store(c, k_pe, positions, cos_sin, slot_mapping, kv_pages, ...)  rotated keys -> latent cache
+  sparse_latent_attention(q, kv_pages, slots, scale, ...)                 attention over selected slots
+  paged_latent_attention(q, kv_pages, block_table, seq_lens, R, scale, ...)  over all cached tokens
 
 q/k are fp8 e4m3fn bytes (torch.uint8 or torch.float8_e4m3fn), s/w float32,
 ks/ke/block_table/seq_lens int32.
@@ -31,9 +34,11 @@ H = 32
 D = 128
 MAX_TOPK = 2048
 PAGE_SIZE = 64
+LATENT = 512   # latent values a token (the latent attention's keys and values)
+ROPE = 64      # rotated key values a token
 
 OK, EINVAL, EUNSUPPORTED, EWORKSPACE, ECUDA = 0, 1, 2, 3, 4
-STATUS_WAIT_TIMEOUT, STATUS_BAD_PAGE, STATUS_SEQ_TOO_LONG = 1, 2, 4
+STATUS_WAIT_TIMEOUT, STATUS_BAD_PAGE, STATUS_SEQ_TOO_LONG, STATUS_BAD_SLOT = 1, 2, 4, 16
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8idx.so")
@@ -79,10 +84,22 @@ def lib() -> ctypes.CDLL:
             L.fp8idx_prepare_ragged.argtypes = [vp, vp, vp, i32, vp, i64, i64, vp, vp, vp, i64, vp, i64,
                                                 vp]
             L.fp8idx_topk_transform.argtypes = [vp, i64, i32, vp, vp, i32, vp, i64, i64, i32, vp, vp]
+            f32 = ctypes.c_float
+            L.fp8idx_latent_store.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i32, vp, i64, vp, vp, vp,
+                                              vp, i64, i64, vp, i64, i64, i32, vp]
+            L.fp8idx_sparse_latent_attention_workspace.argtypes = [i64, i32, i32]
+            L.fp8idx_sparse_latent_attention_workspace.restype = sz
+            L.fp8idx_sparse_latent_attention.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, i64, i64, i32, i32, i32,
+                                                         i32, f32, vp, vp, vp, sz, vp]
+            L.fp8idx_paged_latent_attention_workspace.argtypes = [i64, i32, i32, i32]
+            L.fp8idx_paged_latent_attention_workspace.restype = sz
+            L.fp8idx_paged_latent_attention.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, i64, i32, i32, i64, i32,
+                                                        i32, i32, i32, f32, vp, vp, vp, sz, vp]
             for name in ("fp8idx_mqa_logits", "fp8idx_topk_rows", "fp8idx_mqa_logits_topk",
                          "fp8idx_paged_mqa_logits_topk", "fp8idx_paged_mqa_logits_topk_slots",
                          "fp8idx_read_device_status",
-                         "fp8idx_act_quant_store", "fp8idx_prepare_ragged", "fp8idx_topk_transform"):
+                         "fp8idx_act_quant_store", "fp8idx_prepare_ragged", "fp8idx_topk_transform",
+                         "fp8idx_latent_store", "fp8idx_sparse_latent_attention", "fp8idx_paged_latent_attention"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -335,3 +352,183 @@ def topk_transform(idx, page_table, page_size: int = 1, row_base=None, row_table
                                        rows_per_table_row, _ptr(page_table), page_table.shape[0],
                                        page_table.stride(0), page_size, _ptr(out), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------- latent attention
+
+def _rows(t: torch.Tensor, name: str, width: int, dim: int, device=None) -> torch.Tensor:
+    """A bf16 CUDA tensor [..., width] with `dim` dimensions whose last is dense (outer strides are free)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != dim or t.shape[-1] != width:
+        raise ValueError(f"{name} must have {dim} dimensions, the last of {width}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _pool(kv_pages, s_pages, pe_pages):
+    """Checks a latent pool; returns its page count."""
+    if (s_pages is None) != (pe_pages is None):
+        raise ValueError("an fp8 pool has both s_pages and pe_pages, a bf16 pool neither")
+    if s_pages is None:
+        _dev(kv_pages, "kv_pages", torch.bfloat16)
+        width = LATENT + ROPE
+    else:
+        _bytes(kv_pages, "kv_pages")
+        _dev(s_pages, "s_pages", torch.float32)
+        _dev(pe_pages, "pe_pages", torch.bfloat16)
+        width = LATENT
+    if kv_pages.dim() != 3 or kv_pages.shape[2] != width:
+        raise ValueError(f"kv_pages must be [pages, {PAGE_SIZE}, {width}], got {tuple(kv_pages.shape)}")
+    pages = kv_pages.shape[0]
+    if s_pages is not None and (s_pages.numel() != pages * kv_pages.shape[1]
+                                or tuple(pe_pages.shape) != (pages, kv_pages.shape[1], ROPE)):
+        raise ValueError("kv_pages, s_pages and pe_pages disagree")
+    _same_device(kv_pages.device, s_pages=s_pages, pe_pages=pe_pages)
+    return pages
+
+
+def latent_store(c, k_pe, positions, cos_sin, slot_mapping, kv_pages, s_pages=None, pe_pages=None, q_pe=None,
+                 q_out=None, interleaved: bool = True, stream=None):
+    """New tokens into the paged latent cache, in place, with the rotation applied on the way.
+
+    c [T, 512] and k_pe [T, 64] bfloat16 (row strides are free: both may be
+    parts of one projection output); positions and slot_mapping [T] int64;
+    cos_sin [max_pos, 64] float32 (32 cosines, then 32 sines).  bf16 pool:
+    kv_pages [P, 64, 576] bfloat16.  fp8 pool: kv_pages [P, 64, 512] uint8 or
+    float8_e4m3fn, s_pages [P, 64] float32, pe_pages [P, 64, 64] bfloat16.
+    q_pe [T, H, 64] and q_out (the same shape): the queries' rotary part,
+    rotated by the same angles.  interleaved: pairs (2i, 2i + 1), else
+    (i, 32 + i).  A slot outside the pool is not stored; a token whose
+    position is outside the table is left out.  Returns the pool tensors.
+    """
+    _pool(kv_pages, s_pages, pe_pages)
+    dev = kv_pages.device
+    if kv_pages.shape[1] != PAGE_SIZE:
+        raise ValueError(f"page size must be {PAGE_SIZE}, got {kv_pages.shape[1]}")
+    c = _rows(c, "c", LATENT, 2, dev)
+    k_pe = _rows(k_pe, "k_pe", ROPE, 2, dev)
+    positions = _dev(positions, "positions", torch.int64)
+    slot_mapping = _dev(slot_mapping, "slot_mapping", torch.int64)
+    cos_sin = _dev(cos_sin, "cos_sin", torch.float32)
+    _same_device(dev, positions=positions, slot_mapping=slot_mapping, cos_sin=cos_sin)
+    T = c.shape[0]
+    if k_pe.shape[0] != T or positions.numel() != T or slot_mapping.numel() != T:
+        raise ValueError("c, k_pe, positions and slot_mapping must have one entry per token")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != ROPE:
+        raise ValueError(f"cos_sin must be [max_pos, {ROPE}]")
+    if (q_pe is None) != (q_out is None):
+        raise ValueError("q_pe and q_out go together")
+    qs = (None, 0, 0, None, 0, 0, 1)
+    if q_pe is not None:
+        q_pe = _rows(q_pe, "q_pe", ROPE, 3, dev)
+        q_out = _rows(q_out, "q_out", ROPE, 3, dev)
+        if q_pe.shape != q_out.shape or q_pe.shape[0] != T:
+            raise ValueError("q_pe and q_out must be [T, H, 64]")
+        qs = (q_pe.data_ptr(), q_pe.stride(0), q_pe.stride(1), q_out.data_ptr(), q_out.stride(0), q_out.stride(1),
+              q_pe.shape[1])
+    with torch.cuda.device(dev):
+        _check(lib().fp8idx_latent_store(c.data_ptr(), c.stride(0), k_pe.data_ptr(), k_pe.stride(0), T,
+                                         positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0],
+                                         1 if interleaved else 0, slot_mapping.data_ptr(),
+                                         kv_pages.shape[0] * PAGE_SIZE, kv_pages.data_ptr(), _ptr(s_pages),
+                                         _ptr(pe_pages), *qs, _stream(stream)))
+    return kv_pages if s_pages is None else (kv_pages, s_pages, pe_pages)
+
+
+def sparse_latent_workspace_size(rows: int, heads: int, topk: int) -> int:
+    return int(lib().fp8idx_sparse_latent_attention_workspace(rows, heads, topk))
+
+
+def paged_latent_workspace_size(B: int, R: int, max_blocks: int, heads: int) -> int:
+    return int(lib().fp8idx_paged_latent_attention_workspace(B, R, max_blocks, heads))
+
+
+def _attn_outputs(q, out, lse, return_lse):
+    rows, heads = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((rows, heads, LATENT), dtype=torch.bfloat16, device=q.device)
+    elif tuple(_dev(out, "out", torch.bfloat16).shape) != (rows, heads, LATENT):
+        raise ValueError(f"out must be [{rows}, {heads}, {LATENT}]")
+    if lse is None:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    elif tuple(_dev(lse, "lse", torch.float32).shape) != (rows, heads):
+        raise ValueError(f"lse must be [{rows}, {heads}]")
+    _same_device(q.device, out=out, lse=lse)
+    return out, lse
+
+
+def sparse_latent_attention(q, kv_pages, slots, scale: float, s_pages=None, pe_pages=None, out=None, lse=None,
+                            workspace=None, return_lse: bool = False, stream=None):
+    """Absorbed latent attention of every row over its selected pool slots.
+
+    q [rows, H, 576] bfloat16 (row and head strides are free); slots
+    [rows, topk] int32 physical slots, entries below 0 skipped (what
+    paged_mqa_logits_topk(slots=True) and topk_transform give); the pool as in
+    latent_store.  Returns out [rows, H, 512] bfloat16, and with return_lse
+    the log of each row's sum, [rows, H] float32.  A row without slots gives
+    0 and -inf.
+    """
+    q = _rows(q, "q", LATENT + ROPE, 3)
+    pages = _pool(kv_pages, s_pages, pe_pages)
+    if not isinstance(slots, torch.Tensor) or not slots.is_cuda or slots.dtype != torch.int32:
+        raise TypeError("slots must be an int32 CUDA tensor")
+    if slots.dim() != 2 or slots.shape[0] != q.shape[0]:
+        raise ValueError("slots must be [rows, topk]")
+    topk = slots.shape[1]
+    if topk > 1 and slots.stride(1) != 1:
+        raise ValueError("slots must have unit column stride")
+    _same_device(q.device, kv_pages=kv_pages, slots=slots, workspace=workspace)
+    out, lse = _attn_outputs(q, out, lse, return_lse)
+    rows, heads = q.shape[0], q.shape[1]
+    ld = max(slots.stride(0), topk) if rows <= 1 else slots.stride(0)
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            workspace = alloc_workspace(sparse_latent_workspace_size(rows, heads, topk), q.device)
+        _check(lib().fp8idx_sparse_latent_attention(
+            q.data_ptr(), q.stride(0), q.stride(1), kv_pages.data_ptr(), _ptr(s_pages), _ptr(pe_pages),
+            pages * kv_pages.shape[1], slots.data_ptr(), ld, rows, topk, heads, LATENT, ROPE, scale, out.data_ptr(),
+            _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return (out, lse) if return_lse else out
+
+
+def paged_latent_attention(q, kv_pages, block_table, seq_lens, R: int, scale: float, s_pages=None, pe_pages=None,
+                           out=None, lse=None, workspace=None, return_lse: bool = False, stream=None):
+    """Absorbed latent attention of R rows per request over all its cached tokens.
+
+    q [B * R, H, 576] bfloat16 (row and head strides are free); keys through
+    a 64-token block table [B, max_blocks] int32; row t of a request of length
+    L = seq_lens[b] sees keys [0, L - R + t + 1).  Pool and results as in
+    sparse_latent_attention.
+    """
+    q = _rows(q, "q", LATENT + ROPE, 3)
+    pages = _pool(kv_pages, s_pages, pe_pages)
+    block_table = _dev(block_table, "block_table", torch.int32)
+    seq_lens = _dev(seq_lens, "seq_lens", torch.int32)
+    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [B, max_blocks] and seq_lens [B]")
+    B, max_blocks = block_table.shape
+    if q.shape[0] != B * R:
+        raise ValueError(f"q has {q.shape[0]} rows, expected B*R = {B * R}")
+    _same_device(q.device, kv_pages=kv_pages, block_table=block_table, seq_lens=seq_lens, workspace=workspace)
+    out, lse = _attn_outputs(q, out, lse, return_lse)
+    heads = q.shape[1]
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            workspace = alloc_workspace(paged_latent_workspace_size(B, R, max_blocks, heads), q.device)
+        _check(lib().fp8idx_paged_latent_attention(
+            q.data_ptr(), q.stride(0), q.stride(1), kv_pages.data_ptr(), _ptr(s_pages), _ptr(pe_pages),
+            block_table.data_ptr(), seq_lens.data_ptr(), B, R, max_blocks, pages, kv_pages.shape[1], heads, LATENT,
+            ROPE, scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return (out, lse) if return_lse else out

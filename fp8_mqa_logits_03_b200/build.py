@@ -4,13 +4,25 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8idx.so")
-SOURCES = ["kernels.cu", "quant.cu", "index_prep.cu", "api.cu"]
-DEPS = SOURCES + ["kernels.cuh", "ptx.cuh", "select.cuh"]
+SOURCES = ["kernels.cu", "quant.cu", "index_prep.cu", "latent_store.cu", "latent.cu", "latent_api.cu", "api.cu"]
+DEPS = SOURCES + ["api_common.h", "kernels.cuh", "latent.cuh", "ptx.cuh", "select.cuh", "wait.cuh"]
 HEADER = os.path.join(os.path.dirname(HERE), "include", "fp8idx.h")
+# the headers each source includes (its object is rebuilt when one changes)
+INCLUDES = {
+    "kernels.cu": ["kernels.cuh", "ptx.cuh", "select.cuh", "wait.cuh"],
+    "quant.cu": ["ptx.cuh"],
+    "index_prep.cu": ["ptx.cuh"],
+    "latent_store.cu": ["latent.cuh", "kernels.cuh"],
+    "latent.cu": ["latent.cuh", "kernels.cuh", "ptx.cuh", "wait.cuh"],
+    "latent_api.cu": ["api_common.h", "kernels.cuh", "latent.cuh"],
+    "api.cu": ["api_common.h", "kernels.cuh"],
+}
 
 
 def nvcc_path() -> str:
@@ -20,26 +32,42 @@ def nvcc_path() -> str:
     return cand
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target: str, deps) -> bool:
+    """Whether `target` is missing or older than one of `deps`."""
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    srcs = [os.path.join(CSRC, f) for f in DEPS] + [HEADER]
-    return any(os.path.getmtime(s) > t for s in srcs)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _stale() -> bool:
+    return _newer(LIB, [os.path.join(CSRC, f) for f in DEPS] + [HEADER])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu into libfp8idx.so (static cudart, no libcuda link)."""
+    """Compile csrc/*.cu (in parallel) into libfp8idx.so (static cudart, no libcuda link)."""
     if not force and not _stale():
         return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), "-std=c++17", "-O3", "-lineinfo",
-           "-gencode", "arch=compute_100a,code=sm_100a",
-           "-Xcompiler", "-fPIC", "-shared", "-cudart", "static",
-           "-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
+    os.makedirs(OBJ, exist_ok=True)
+    flags = ["-std=c++17", "-O3", "-lineinfo", "-gencode", "arch=compute_100a,code=sm_100a",
+             "-Xcompiler", "-fPIC"]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd, cwd=HERE)
+        flags.insert(0, "-Xptxas=-v")
+
+    def compile_one(src: str) -> str:
+        obj = os.path.join(OBJ, src + ".o")
+        deps = [os.path.join(CSRC, f) for f in [src] + INCLUDES[src]] + [HEADER, os.path.abspath(__file__)]
+        if force or _newer(obj, deps):
+            tmp = obj + f".tmp{os.getpid()}.o"
+            subprocess.check_call([nvcc_path(), *flags, "-c", "-o", tmp, os.path.join(CSRC, src)], cwd=HERE)
+            os.replace(tmp, obj)
+        return obj
+
+    with ThreadPoolExecutor(len(SOURCES)) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
+    tmp = LIB + f".tmp{os.getpid()}"
+    subprocess.check_call([nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-Xcompiler", "-fPIC",
+                           "-shared", "-cudart", "static", "-o", tmp, *objs], cwd=HERE)
     os.replace(tmp, LIB)
     return LIB
 

@@ -5,14 +5,12 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <string>
 
 #include "../../include/fp8idx.h"
+#include "api_common.h"
 #include "kernels.cuh"
 
 namespace fp8idx {
@@ -42,42 +40,6 @@ cudaError_t launch_topk_transform(const int32_t* idx, int64_t rows, int topk, co
 namespace {
 
 using namespace fp8idx;
-
-thread_local std::string t_last_error;
-unsigned long long g_wait_limit_ns = 2000000000ull;
-int g_debug_withhold = 0;
-
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  t_last_error = buf;
-  return code;
-}
-
-int ok() {
-  t_last_error.clear();
-  return FP8IDX_OK;
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(FP8IDX_ECUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-
-int device_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return sms;
-}
 
 // ---------------------------------------------------------------- TMA descriptors
 
@@ -364,12 +326,6 @@ int resolve_status_source(const void* ws, const void** src) {
   }
   return FP8IDX_OK;
 }
-
-#define FP8IDX_TRY(x)          \
-  do {                         \
-    int _rc = (x);             \
-    if (_rc != FP8IDX_OK) return _rc; \
-  } while (0)
 
 int check_prefill_inputs(const uint8_t* q, const uint8_t* k, const float* s, const float* w,
                          const int32_t* ks, const int32_t* ke, int64_t m, int64_t n) {

@@ -66,7 +66,8 @@ enum {
   FP8IDX_STATUS_WAIT_TIMEOUT = 1,   /* a pipeline wait gave up; outputs are invalid      */
   FP8IDX_STATUS_BAD_PAGE = 2,       /* a block-table entry outside [0, num_pages)        */
   FP8IDX_STATUS_SEQ_TOO_LONG = 4,   /* seq_lens[b] > max_blocks * page_size (clamped)    */
-  FP8IDX_STATUS_CAND_OVERFLOW = 8   /* internal: a candidate was dropped; outputs invalid */
+  FP8IDX_STATUS_CAND_OVERFLOW = 8,  /* internal: a candidate was dropped; outputs invalid */
+  FP8IDX_STATUS_BAD_SLOT = 16       /* a selected slot at or past num_slots (left out)   */
 };
 
 /*
@@ -255,6 +256,88 @@ int fp8idx_prepare_ragged(const int32_t* seq_len, const int32_t* q_len, const in
 int fp8idx_topk_transform(const int32_t* idx, int64_t rows, int topk, const int32_t* row_base,
                           const int32_t* row_table, int rows_per_table_row, const int32_t* page_table,
                           int64_t table_rows, int64_t ld_table, int page_size, int32_t* out, void* stream);
+
+/*
+ * New tokens into the paged latent cache: the pool that the latent attention
+ * below reads.  A token's entry is its latent vector c[t] (512 values, which
+ * are both its key and its value) and its key part k_pe[t] (64 values)
+ * rotated by the token's position; the queries' rotary part is rotated by
+ * the same angles in the same launch when q_pe is not NULL.  With n =
+ * positions[t] and, for i < 32, (cos, sin) = cos_sin[n][i], cos_sin[n][32+i]:
+ *     (a, b) = (x[2i], x[2i+1])  if interleaved != 0, else (x[i], x[32+i])
+ *     a' = a cos - b sin,  b' = b cos + a sin      (fp32, rounded once to bf16)
+ * Token t goes to pool slot slot[t] (page slot / 64, row slot % 64); a slot
+ * outside [0, num_slots) is not stored (its q_pe row is still rotated).  A
+ * token whose position is outside [0, max_pos) is left out altogether.
+ *   c, k_pe    [T, 512], [T, 64] bf16 bit patterns with their row strides in
+ *              values (both may be parts of one [T, 576] buffer)
+ *   positions, slot  [T] int64          cos_sin  [max_pos, 64] fp32
+ *   bf16 pool: kv_pool [num_slots, 576] bf16 (latent, then the rotated part),
+ *              s_pool = pe_pool = NULL
+ *   fp8 pool:  kv_pool [num_slots, 512] e4m3 codes, s_pool [num_slots] fp32,
+ *              pe_pool [num_slots, 64] bf16; the codes and the scale follow
+ *              fp8idx_act_quant_store's rule over the 512 latent values
+ *              (s = max(max |c|, 1e-4) / 448, NaN left out of the maximum)
+ *   q_pe, q_out  [T, H, 64] bf16 with row and head strides in values, H in
+ *              [1, 128]; q_out may be q_pe itself, and otherwise must not
+ *              overlap it (it is usually the last 64 of the [T, H, 576]
+ *              absorbed queries)
+ * Every bf16 pointer and stride must be a multiple of 16 bytes.  Slots that
+ * no token names are left untouched; two tokens naming one slot race.
+ * No workspace.
+ */
+int fp8idx_latent_store(const uint16_t* c, int64_t c_stride, const uint16_t* k_pe, int64_t k_pe_stride, int64_t T,
+                        const int64_t* positions, const float* cos_sin, int64_t max_pos, int interleaved,
+                        const int64_t* slot, int64_t num_slots, void* kv_pool, float* s_pool, uint16_t* pe_pool,
+                        const uint16_t* q_pe, int64_t q_row_stride, int64_t q_head_stride, uint16_t* q_out,
+                        int64_t out_row_stride, int64_t out_head_stride, int H, void* stream);
+
+/*
+ * Latent attention over selected slots (absorbed form): the sparse attention
+ * that follows the indexer, reading the slots that
+ * fp8idx_paged_mqa_logits_topk_slots or fp8idx_topk_transform wrote.  With
+ * k[j] the 576 values of pool slot j (fp8 pool: codes x scale, then the
+ * rotated part), for every row i and head h:
+ *     x[j]   = scale * sum_{d<576} q[i,h,d] * k[j,d]     over the slots j = slots[i, :] >= 0
+ *     out[i,h,:] = sum_j softmax(x)[j] * k[j, 0:512],   lse[i,h] = log sum_j exp(x[j])
+ * A row without slots gives 0 and -inf.  A slot named twice counts twice.
+ * Negative entries are skipped wherever they stand; a slot at or past
+ * num_slots is left out and sets BAD_SLOT.  The products are exact with fp32
+ * sums; the softmax weights are rounded to bf16 for the value product, the
+ * sum that divides them is not.
+ *   q          [rows, H, 576] bf16, row and head strides in values (multiples
+ *              of 16 bytes), H in [1, 128]; latent must be 512 and rope 64
+ *   pool       as fp8idx_latent_store, num_slots < 2^31
+ *   slots      [rows, topk] int32, row stride ld_slots
+ *   out        [rows, H, 512] bf16          lse  [rows, H] fp32 or NULL
+ *   scale      positive and finite
+ * ws / ws_bytes: as for fp8idx_mqa_logits_topk, of at least
+ * fp8idx_sparse_latent_attention_workspace(rows, H, topk) bytes.
+ */
+size_t fp8idx_sparse_latent_attention_workspace(int64_t rows, int H, int topk);
+int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,
+                                   const void* kv_pool, const float* s_pool, const uint16_t* pe_pool,
+                                   int64_t num_slots, const int32_t* slots, int64_t ld_slots, int64_t rows, int topk,
+                                   int H, int latent, int rope, float scale, uint16_t* out, float* lse, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/*
+ * Latent attention over all cached tokens (absorbed form, decode / verify):
+ * B requests with R query rows each (1 to 8), keys through the block table as
+ * in fp8idx_paged_mqa_logits_topk: row t of request b sees keys
+ * [0, seq_lens[b] - R + t + 1).  Values, formulas and pool as above; a page
+ * entry outside [0, num_pages) sets BAD_PAGE and its keys are left out, a
+ * length beyond max_blocks * 64 is clamped and sets SEQ_TOO_LONG.  What the
+ * pool holds past a request's length never reaches the outputs, NaN included.
+ *   q  [B * R, H, 576] bf16 with strides    block_table  [B, max_blocks] int32
+ *   seq_lens [B] int32                      out, lse     [B * R, H, ...] as above
+ */
+size_t fp8idx_paged_latent_attention_workspace(int64_t B, int R, int max_blocks, int H);
+int fp8idx_paged_latent_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,
+                                  const void* kv_pages, const float* s_pages, const uint16_t* pe_pages,
+                                  const int32_t* block_table, const int32_t* seq_lens, int64_t B, int R,
+                                  int max_blocks, int64_t num_pages, int page_size, int H, int latent, int rope,
+                                  float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Tests and diagnostics.  fp8idx_read_device_status synchronises `stream`
