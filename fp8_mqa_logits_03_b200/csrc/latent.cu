@@ -22,11 +22,13 @@
 //              four lanes a head), running maximum and sum in registers,
 //              weights as bf16 into shared memory; at a group's end they read
 //              the sums from TMEM, divide and write.
-//   warps 4-7  producers: gather the tile's key rows into one of two stages
-//              with 16-byte asynchronous copies in the 128-byte swizzle.
-//   warp 8     one thread issues the MMAs, whichever is ready: a group of
-//              score products as its part of the tile lands, or the value
-//              product of a tile whose weights are ready.
+//   warps 4-11 producers: gather the tile's key rows, one tile ahead, into
+//              registers (16-byte loads), and write them in the 128-byte
+//              swizzle into one of two stages as it comes free; fp8 codes
+//              become bf16 on the way, exactly, and the scales go to the
+//              softmax warps.
+//   warp 12    issues the score products, part by part as a tile lands.
+//   warp 13    issues the value products.
 // Scores: M = 64 columns, N = 64 keys, K = 576.  Values, transposed so that
 // the sums of all 512 values fit in half of TMEM: M = 128 values (the same
 // key rows read as an MN-major operand), N = 64 columns, K = 64 keys.
@@ -47,16 +49,18 @@ constexpr int kChunkBytes = kAttnKeys * 128;    // [64 keys][64 values] bf16, sw
 constexpr int kStageBytes = kChunks * kChunkBytes;
 constexpr int kParts = 5;                       // barriers of a stage: four chunk pairs, and the rotated part
 constexpr int kInfo = 4;                        // tile descriptions in flight
-constexpr int kProducers = 128;
 constexpr int kSoftmax = 128;
-constexpr int kThreads = kSoftmax + kProducers + 32;
+constexpr int kProducers = 256;
+constexpr int kProdWarps = kProducers / 32;
+constexpr int kThreads = kSoftmax + kProducers + 64;
 
 // shared memory, from a 1024-byte boundary
 constexpr int kOffQ = 0;
 constexpr int kOffK = kStageBytes;              // the 64 query columns take as much as a stage
 constexpr int kOffP = kOffK + kStages * kStageBytes;
 constexpr int kOffMisc = kOffP + kChunkBytes;
-constexpr int kSmemBytes = kOffMisc + 2048 + 1024;
+constexpr int kMiscBytes = 3072;
+constexpr int kSmemBytes = kOffMisc + kMiscBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
 // TMEM columns
@@ -86,13 +90,14 @@ struct Misc {
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full, pv_done, drain;
   Info info[kInfo];
+  float scale[kInfo][kAttnKeys];  // fp8: the tile's key scales (0 for a key that does not exist)
   float stat_m[kAttnCols], stat_l[kAttnCols];
   uint32_t tmem;
   int abort_flag;
   int scan[kThreads / 32 + 1];
   int start_group, start_tile;
 };
-static_assert(sizeof(Misc) <= 2048, "misc");
+static_assert(sizeof(Misc) <= kMiscBytes, "misc");
 
 // ---------------------------------------------------------------- PTX
 
@@ -170,6 +175,27 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // (tensor core) reads of the same shared memory.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(reinterpret_cast<uint64_t>(p)));
+  return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Bytes `2 i` and `2 i + 1` of w as a bf16 pair, exactly: an e4m3 code shifted
+// into bf16's exponent and mantissa is its value times 2^-120 (subnormals
+// included), and the product with 2^120 is exact.
+__device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t w, int i) {
+  const uint32_t t = __byte_perm(w, 0, i == 0 ? 0x1404 : 0x3424);  // codes in the upper bytes of the halves
+  uint32_t v = ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x7B807B80u));
+  return v;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -187,6 +213,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xFFFFFFFFu, wait_phase<kSpin>(bar, parity, abort_flag, status, limit_ns));
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- schedule
 
 // Tiles of group g: at least one, so that an empty group is written too.
@@ -202,10 +239,9 @@ __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kAttnKey
 
 // ---------------------------------------------------------------- the kernel
 
-template <bool PAGED>
+template <bool PAGED, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_constant__ LatentAttnParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cg = blockIdx.x % p.ncg, part = blockIdx.x / p.ncg;
@@ -215,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s)
       for (int i = 0; i < kParts; ++i) {
-        mbar_init(&ms.full[s][i], kProducers + (i == 0 ? 1 : 0));  // part 0 also announces the tile's description
+        mbar_init(&ms.full[s][i], kProdWarps);
         mbar_init(&ms.empty[s][i], 1);
       }
     mbar_init(&ms.q_full, kProducers);
@@ -225,12 +261,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     }
     mbar_init(&ms.p_full, kSoftmax);
     mbar_init(&ms.pv_done, 1);
-    mbar_init(&ms.drain, 1);
+    mbar_init(&ms.drain, 2);
     ms.abort_flag = 0;
     fence_mbar_init();
     p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (warp == 8) {
+  if (warp == 12) {
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
@@ -286,13 +322,27 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   const int64_t x1 = part < parts ? (part + 1) * total / parts : 0;
   const uint32_t tbase = ms.tmem;
 
-  if (warp >= 4 && warp < 8) {
+  if (warp >= 4 && warp < 12) {
     // ================================================================ producers
     const int pt = tid - kSoftmax;
-    const int piece = pt & 7, r0 = pt >> 3;  // 16-byte piece of a chunk row; rows r0 + 16 k
-    const uint32_t dst0 = smem_u32(smem + kOffK) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
-    const uint32_t qdst0 = smem_u32(smem + kOffQ) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
-    int g, t;
+    const int piece = pt & 7, r0 = pt >> 3;  // 16-byte piece of a chunk row; rows r0 and r0 + 32
+    const uint32_t row_dst = smem_u32(smem + kOffK) + r0 * 128;
+    const uint32_t swz = (piece ^ (r0 & 7)) << 4;
+    // fp8: 16 codes become pieces 2 (piece % 4) and the next of chunk piece / 4;
+    // lanes of the second chunk write the odd piece first, so that the eight
+    // lanes of a row hit eight different 16-byte bank groups
+    const int odd = piece >> 2, sub = 2 * (piece & 3);
+    const uint32_t fdst0 = odd * kChunkBytes + (((sub + odd) ^ (r0 & 7)) << 4);
+    const uint32_t fdst1 = odd * kChunkBytes + (((sub + 1 - odd) ^ (r0 & 7)) << 4);
+    constexpr int kRowBytes = FP8 ? kLatent : kLatentDim * 2;
+
+    // ---- where the stream stands: the next tile to look at is tile t of group g
+    int g, t, te = 0, len = 0, slot = 0;
+    bool direct = false, fresh = true;  // fresh: no tile of the segment has been emitted
+    int64_t x = x0;                     // end of the current segment on the tile axis
+    const int32_t* list = nullptr;
+    int bad = 0;
+    int next_idx[2] = {-1, -1};         // its raw list entries of keys lane and lane + 32 (paged: the page)
     if (PAGED) {
       g = ms.start_group;
       t = ms.start_tile;
@@ -301,238 +351,303 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       g = static_cast<int>(x0 / per);
       t = static_cast<int>(x0 - static_cast<int64_t>(g) * per);
     }
-    int i = 0;           // tiles emitted
-    bool ok = true;
-    int bad = 0;
-    for (int64_t x = x0; x < x1 && ok; ++g, t = 0) {
-      // ---- a segment: tiles [t, te) of group g
-      const int len = group_len<PAGED>(p, g);
+    // Starts the segment of group g at tile t.
+    auto open_segment = [&]() {
+      len = group_len<PAGED>(p, g);
       const int nt = tiles_of(len);
-      const int te = static_cast<int>(min(static_cast<int64_t>(nt), t + (x1 - x)));
-      const bool direct = t == 0 && te == nt;
-      const int slot = (blockIdx.x * 2 + (t == 0 ? 1 : 0));
-      bool first = true;
+      te = static_cast<int>(min(static_cast<int64_t>(nt), t + (x1 - x)));
+      direct = t == 0 && te == nt;
+      slot = blockIdx.x * 2 + (t == 0 ? 1 : 0);
+      fresh = true;
       if (t == 0 && te < nt && pt == 0) {
         // the group goes on in the ranges after this one, up to the one that holds its last tile
         const int64_t last = x + nt - 1;
         const int c1 = static_cast<int>(((last + 1) * parts - 1) / total);
         p.meta[blockIdx.x] = make_int4(g, c1 - part + 1, 0, 0);
       }
-      const int32_t* list = PAGED ? p.block_table + static_cast<int64_t>(g) * p.max_blocks
-                                  : p.slots + static_cast<int64_t>(g) * p.ld_slots;
+      list = PAGED ? p.block_table + static_cast<int64_t>(g) * p.max_blocks
+                   : p.slots + static_cast<int64_t>(g) * p.ld_slots;
       x += te - t;
-      for (; t < te; ++t) {
-        // ---- the tile's rows: slot of key `lane` and `lane + 32`, -1 where there is none
-        int64_t sl[2];
+    };
+    auto fetch_idx = [&]() {
+      if (PAGED) {
+        next_idx[0] = t * kAttnKeys < len ? __ldg(list + t) : -1;  // a tile is a page
+      } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int j = t * kAttnKeys + h * 32 + lane;
+          next_idx[h] = j < len ? __ldg(list + j) : -1;
+        }
+      }
+    };
+
+    // ---- the tile about to be written, its rows on the way in registers
+    Info d;
+    uint4 raw[FP8 ? 10 : 18];
+    float sc = 0.f;
+    const uint8_t* src[2];
+    const uint8_t* pe_src[2];
+    bool have[2];
+    // Finds the next tile that holds keys (or ends a segment, or the stream) and describes it in d.
+    auto advance = [&]() {
+      for (;;) {
+        if (t == te) {
+          if (x == x1) {
+            d.flags = kEnd;
+            return;
+          }
+          ++g;
+          t = 0;
+          open_segment();
+          fetch_idx();
+        }
+        int64_t sl[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           int64_t v = -1;
-          if (j < len) {
-            if (PAGED) {
-              const int pg = __ldg(list + t);  // a tile is a page
+          if (PAGED) {
+            const int pg = next_idx[0];
+            if (t * kAttnKeys + h * 32 + lane < len) {
               if (pg >= 0 && pg < p.num_slots / kPageSize) v = static_cast<int64_t>(pg) * kPageSize + h * 32 + lane;
               else bad |= kStatusBadPage;
-            } else {
-              v = __ldg(list + j);
-              if (v >= p.num_slots) {
-                v = -1;
-                bad |= kStatusBadSlot;
-              }
+            }
+          } else {
+            v = next_idx[h];
+            if (v >= p.num_slots) {
+              v = -1;
+              bad |= kStatusBadSlot;
             }
           }
           sl[h] = v;
         }
-        const unsigned long long mask =
-            __ballot_sync(0xFFFFFFFFu, sl[0] >= 0) |
-            (static_cast<unsigned long long>(__ballot_sync(0xFFFFFFFFu, sl[1] >= 0)) << 32);
-        const bool last = t == te - 1;
-        const bool null = mask == 0;
+        d.mask = __ballot_sync(0xFFFFFFFFu, sl[0] >= 0) |
+                 (static_cast<unsigned long long>(__ballot_sync(0xFFFFFFFFu, sl[1] >= 0)) << 32);
+        const bool last = t == te - 1, null = d.mask == 0;
+        d.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (null ? kNull : 0) | (direct ? kDirect : 0);
+        d.group = g;
+        d.ends = PAGED ? len - p.R + 1 - t * kAttnKeys : 1 << 20;
+        d.piece = slot;
+        ++t;
+        if (t < te) fetch_idx();
         if (null && !last) continue;  // nothing to do and nothing to say
-        const int st = i & 1;
-        const uint32_t ph = (i >> 1) & 1;
-        // ---- describe the tile.  The entry was tile i - 4's; the values of
-        // tile i - 2 have begun, so every role is past tile i - 4.
-        if (!warp_wait(&ms.empty[st][0], ph ^ 1, abort_flag, p.status, limit) ||
-            !warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, p.status, limit)) {
+        if (!null) {
+          fresh = false;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int64_t v = __shfl_sync(0xFFFFFFFFu, sl[k], r0);
+            have[k] = v >= 0;
+            src[k] = p.kv + (v >= 0 ? v : 0) * kRowBytes + piece * 16;
+            if (FP8) pe_src[k] = p.pe + (v >= 0 ? v : 0) * (kRope * 2) + piece * 16;
+          }
+          if (FP8 && pt < kAttnKeys) {
+            const int64_t v = pt < 32 ? sl[0] : sl[1];
+            sc = v >= 0 ? __ldg(p.s + v) : 0.f;
+          }
+        }
+        return;
+      }
+    };
+    // Loads of part c (0-3: two chunks; 4: the rotated part) into its registers.
+    auto load_part = [&](int c) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (FP8) {
+          raw[2 * c + k] = have[k] ? ld_stream16(c < 4 ? src[k] + c * 128 : pe_src[k]) : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int u = 0; u < (c < 4 ? 2 : 1); ++u)
+            raw[4 * c + 2 * u + k] = have[k] ? ld_stream16(src[k] + (2 * c + u) * 128) : make_uint4(0, 0, 0, 0);
+        }
+      }
+    };
+    auto store_part = [&](int c, uint32_t dst) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t rd = dst + k * 4096 + 2 * c * kChunkBytes;
+        if (FP8 && c < 4) {
+          const uint4 v = raw[2 * c + k];
+          const uint32_t a[4] = {e4m3_pair_bf16(v.x, 0), e4m3_pair_bf16(v.x, 1), e4m3_pair_bf16(v.y, 0),
+                                 e4m3_pair_bf16(v.y, 1)};
+          const uint32_t b[4] = {e4m3_pair_bf16(v.z, 0), e4m3_pair_bf16(v.z, 1), e4m3_pair_bf16(v.w, 0),
+                                 e4m3_pair_bf16(v.w, 1)};
+          st_shared16(rd + fdst0, odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? b[2] : a[2], odd ? b[3] : a[3]);
+          st_shared16(rd + fdst1, odd ? a[0] : b[0], odd ? a[1] : b[1], odd ? a[2] : b[2], odd ? a[3] : b[3]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < (c < 4 ? 2 : 1); ++u) {
+            const uint4 v = raw[FP8 ? 2 * c + k : 4 * c + 2 * u + k];
+            st_shared16(rd + u * kChunkBytes + swz, v.x, v.y, v.z, v.w);
+          }
+        }
+      }
+    };
+
+    bool ok = true;
+    if (x < x1) {
+      open_segment();
+      fetch_idx();
+    } else {
+      t = te;
+    }
+    advance();
+    if (!(d.flags & (kNull | kEnd))) {
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) load_part(c);
+    }
+    for (int i = 0;; ++i) {
+      const int st = i & 1;
+      const uint32_t ph = (i >> 1) & 1;
+      const int flags = d.flags;
+      const bool null = flags & (kNull | kEnd);
+      if ((flags & kFirst) && !null) {
+        // ---- the group's query columns; their place is free once the last tile's scores are done
+        if (i > 0 && !warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, p.status, limit)) {
           ok = false;
           break;
         }
-        if (pt == 0) {
-          Info& f = ms.info[i & (kInfo - 1)];
-          f.mask = mask;
-          f.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (null ? kNull : 0) | (direct ? kDirect : 0);
-          f.group = g;
-          f.ends = PAGED ? len - p.R + 1 - t * kAttnKeys : 1 << 20;
-          f.piece = slot;
-          mbar_arrive(&ms.full[st][0]);
-        }
-        if (null) {
+        const int cols = p.R * p.H;
 #pragma unroll
-          for (int c = 0; c < kParts; ++c) {
-            if (c > 0 && c < 4 && !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
-            mbar_arrive(&ms.full[st][c]);
-          }
-          if (!ok) break;
-          ++i;
-          continue;
+        for (int k = 0; k < 2; ++k) {
+          const int col = cg * kAttnCols + r0 + 32 * k;
+          const bool v = col < cols;
+          const int row = v ? col / p.H : 0, h = v ? col - row * p.H : 0;
+          const uint8_t* qs = reinterpret_cast<const uint8_t*>(
+              p.q + (static_cast<int64_t>(d.group) * p.R + row) * p.q_row + h * p.q_head);
+          const uint32_t qd = smem_u32(smem + kOffQ) + (r0 + 32 * k) * 128 + swz;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            cp_async16(qd + c * kChunkBytes, qs + c * 128 + piece * 16, v ? 16 : 0);
         }
-        if (first) {
-          // ---- the group's query columns; free once the last tile's scores are done
-          if (i > 0 && !warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, p.status, limit)) {
+        cp_async_arrive(&ms.q_full);
+      }
+      // ---- describe the tile.  The entry was tile i - 4's; the values of
+      // tile i - 2 have begun, so every role is past tile i - 4.
+      if (!warp_wait(&ms.empty[st][0], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
+      if (pt == 0) ms.info[i & (kInfo - 1)] = d;
+      if (FP8 && pt < kAttnKeys) ms.scale[i & (kInfo - 1)][pt] = sc;
+      const bool withhold = p.debug_withhold_first_tile && i == 0;
+      if (null) {
+#pragma unroll 1
+        for (int c = 0; c < kParts; ++c) {
+          if (c > 0 && !(flags & kEnd) && !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) {
             ok = false;
             break;
           }
-          const int cols = p.R * p.H;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int col = cg * kAttnCols + r0 + 16 * k;
-            const bool v = col < cols;
-            const int row = v ? col / p.H : 0, h = v ? col - row * p.H : 0;
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(
-                p.q + (static_cast<int64_t>(g) * p.R + row) * p.q_row + h * p.q_head);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              cp_async16(qdst0 + c * kChunkBytes + k * 2048, src + c * 128 + piece * 16, v ? 16 : 0);
-          }
-          cp_async_arrive(&ms.q_full);
+          __syncwarp();
+          if (lane == 0 && !withhold) mbar_arrive(&ms.full[st][c]);
         }
-        // ---- the key rows
-        const uint8_t* row[4];
-        uint32_t n[4];
+        if (!ok || (flags & kEnd)) break;
+        advance();
+        if (!(d.flags & (kNull | kEnd))) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int64_t v = __shfl_sync(0xFFFFFFFFu, sl[k >> 1], (r0 + 16 * k) & 31);
-          n[k] = v >= 0 ? 16 : 0;
-          row[k] = p.kv + (v >= 0 ? v : 0) * (kLatentDim * 2) + piece * 16;
+          for (int c = 0; c < kParts; ++c) load_part(c);
         }
-        const uint32_t dst = dst0 + st * kStageBytes;
-#pragma unroll
-        for (int c = 0; c < kParts; ++c) {
-          if (c > 0 && c < 4 && !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
-#pragma unroll
-          for (int u = 0; u < (c < 4 ? 2 : 1); ++u) {
-            const int ch = 2 * c + u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) cp_async16(dst + ch * kChunkBytes + k * 2048, row[k] + ch * 128, n[k]);
-          }
-          if (!(p.debug_withhold_first_tile && i == 0 && c == 0)) cp_async_arrive(&ms.full[st][c]);
-        }
-        if (!ok) break;
-        first = false;
-        ++i;
+        continue;
       }
-    }
-    // ---- the end of the stream
-    if (ok) {
-      const int st = i & 1;
-      const uint32_t ph = (i >> 1) & 1;
-      if (warp_wait(&ms.empty[st][0], ph ^ 1, abort_flag, p.status, limit)) {
-        if (pt == 0) {
-          ms.info[i & (kInfo - 1)].flags = kEnd;
-          mbar_arrive(&ms.full[st][0]);
-        }
-        mbar_arrive(&ms.full[st][0]);
+      // ---- write it part by part, and put the next tile's loads in flight behind each
+      advance();
+      const bool more = !(d.flags & (kNull | kEnd));
+      const uint32_t dst = row_dst + st * kStageBytes;
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) {
+        if (c > 0 && !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
+        store_part(c, dst);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0 && !(withhold && c == 0)) mbar_arrive(&ms.full[st][c]);
+        if (more) load_part(c);
       }
+      if (!ok) break;
     }
     cp_async_wait_all();
     if (bad && cg == 0) atomicOr(p.status, bad);
-  } else if (warp == 8) {
-    // ================================================================ MMA
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(64, 64, false), id_v = idesc_bf16_f32(128, 64, true);
-      const uint32_t q_s = smem_u32(smem + kOffQ), k_s = smem_u32(smem + kOffK), p_s = smem_u32(smem + kOffP);
-      int qi = 0, qg = 0, vi = 0, nq = 0;  // next tile and part for scores, next tile for values, query loads seen
-      int qflags = 0;                      // flags of tile qi (known once its part 0 has landed)
-      bool end = false;
-      uint64_t t0 = global_timer_ns();
-      uint32_t polls = 0;
-      while (!(end && vi == qi)) {
-        bool did = false;
-        if (vi < qi && mbar_try_wait(&ms.p_full, vi & 1)) {
-          // ---- values of tile vi
-          const int st = vi & 1;
-          const int f = ms.info[vi & (kInfo - 1)].flags;
-          tc_fence_after();
-          if (f & kNull) {
+  } else if (warp == 12) {
+    // ================================================================ score products
+    // A whole warp runs the issue loops, so that descriptors and branches are
+    // uniform, and one elected lane issues: MMAs issued from a branch on the
+    // lane number took 280 cycles each, elected ones 32 (scores) and 49.
+    constexpr uint32_t id_s = idesc_bf16_f32(64, 64, false);
+    const uint64_t q_d = smem_desc_k128_sw128(smem_u32(smem + kOffQ));
+    int nq = 0;  // query loads seen
+    for (int i = 0;; ++i) {
+      const int st = i & 1;
+      const uint32_t ph = (i >> 1) & 1;
+      const uint64_t k_d = smem_desc_k128_sw128(smem_u32(smem + kOffK + st * kStageBytes));
+      if (!warp_wait(&ms.s_empty[st], ph ^ 1, abort_flag, p.status, limit)) break;
+      if (!warp_wait(&ms.full[st][0], ph, abort_flag, p.status, limit)) break;
+      const int flags = ms.info[i & (kInfo - 1)].flags;
+      if (flags & (kNull | kEnd)) {
+        bool ok = true;
+        for (int c = 1; c < kParts && ok && !(flags & kEnd); ++c)
+          ok = warp_wait(&ms.full[st][c], ph, abort_flag, p.status, limit);
+        if (!ok) break;
+        if (elect_one()) {
+          if (!(flags & kEnd)) mbar_arrive(&ms.empty[st][4]);
+          mbar_arrive(&ms.s_full[st]);
+        }
+        __syncwarp();
+        if (flags & kEnd) break;
+        continue;
+      }
+      if (flags & kFirst) {
+        if (!warp_wait(&ms.q_full, nq & 1, abort_flag, p.status, limit)) break;
+        ++nq;
+        fence_async_shared();  // the queries came by asynchronous copies of other threads
+      }
+      bool ok = true;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) mbar_arrive(&ms.empty[st][c]);
-            mbar_arrive(&ms.pv_done);
-          } else {
+      for (int c = 0; c < kParts; ++c) {
+        if (c > 0 && !warp_wait(&ms.full[st][c], ph, abort_flag, p.status, limit)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t dd = tbase + (FP8 && c == 4 ? kTmemPe : kTmemS) + st * 64;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_bf16(tbase + kTmemO + c * 64,
-                         smem_desc_mn_sw128(k_s + st * kStageBytes + 2 * c * kChunkBytes + ks * 2048),
-                         smem_desc_k128_sw128(p_s + ks * 32), id_v, ks > 0 || !(f & kFirst));
-              mma_commit(&ms.empty[st][c]);
-            }
-            mma_commit(&ms.pv_done);
+          for (int ks = 0; ks < (c < 4 ? 8 : 4); ++ks) {
+            const int off = ((2 * c + (ks >> 2)) * kChunkBytes + (ks & 3) * 32) >> 4;
+            mma_bf16(dd, q_d + off, k_d + off, id_s, ks > 0 || (c > 0 && !(FP8 && c == 4)));
           }
-          ++vi;
-          did = true;
-        } else if (!end) {
-          const int st = qi & 1;
-          const uint32_t ph = (qi >> 1) & 1;
-          if ((qg > 0 || mbar_try_wait(&ms.s_empty[st], ph ^ 1)) && mbar_try_wait(&ms.full[st][qg], ph)) {
-            if (qg == 0) qflags = ms.info[qi & (kInfo - 1)].flags;
-            if (qflags & kEnd) {
-              mbar_arrive(&ms.s_full[st]);
-              end = true;
-            } else if (qflags & kNull) {
-              if (++qg == kParts) {
-                mbar_arrive(&ms.empty[st][4]);
-                mbar_arrive(&ms.s_full[st]);
-                ++qi;
-                qg = 0;
-              }
-            } else {
-              bool go = true;
-              if (qg == 0 && (qflags & kFirst)) {
-                go = wait_phase<kSpin>(&ms.q_full, nq & 1, abort_flag, p.status, limit);
-                ++nq;
-              }
-              if (!go) break;
-              fence_async_shared();
-              tc_fence_after();
-#pragma unroll 1
-              for (int u = 0; u < (qg < 4 ? 2 : 1); ++u) {
-                const int ch = 2 * qg + u;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  mma_bf16(tbase + kTmemS + st * 64, smem_desc_k128_sw128(q_s + ch * kChunkBytes + ks * 32),
-                           smem_desc_k128_sw128(k_s + st * kStageBytes + ch * kChunkBytes + ks * 32), id_s,
-                           ch > 0 || ks > 0);
-              }
-              if (++qg == kParts) {
-                mma_commit(&ms.empty[st][4]);
-                mma_commit(&ms.s_full[st]);
-                ++qi;
-                qg = 0;
-              }
-            }
-            did = true;
+          if (c == 4) {
+            mma_commit(&ms.empty[st][4]);
+            mma_commit(&ms.s_full[st]);
           }
         }
-        if (did) {
-          polls = 0;
-        } else if ((++polls & 63) == 0) {
-          if (polls == 64) t0 = global_timer_ns();
-          if (*abort_flag) break;
-          if (global_timer_ns() - t0 > limit) {
-            *abort_flag = 1;
-            atomicOr(p.status, kStatusWaitTimeout);
-            break;
-          }
-        }
+        __syncwarp();
       }
-      // every MMA issued has finished before shared memory and TMEM go away
-      mma_commit(&ms.drain);
-      const uint64_t td = global_timer_ns();
-      while (!mbar_try_wait(&ms.drain, 0) && global_timer_ns() - td < 200000000ull) {
-      }
+      if (!ok) break;
     }
+    if (elect_one()) mma_commit(&ms.drain);
+    __syncwarp();
+  } else if (warp == 13) {
+    // ================================================================ value products
+    constexpr uint32_t id_v = idesc_bf16_f32(128, 64, true);
+    const uint64_t p_d = smem_desc_k128_sw128(smem_u32(smem + kOffP));
+    for (int i = 0;; ++i) {
+      const int st = i & 1;
+      if (!warp_wait(&ms.p_full, i & 1, abort_flag, p.status, limit)) break;
+      const int flags = ms.info[i & (kInfo - 1)].flags;
+      if (flags & kEnd) break;
+      tc_fence_after();
+      if (elect_one()) {
+        if (flags & kNull) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mbar_arrive(&ms.empty[st][c]);
+          mbar_arrive(&ms.pv_done);
+        } else {
+          const uint64_t v_d = smem_desc_mn_sw128(smem_u32(smem + kOffK + st * kStageBytes));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16(tbase + kTmemO + c * 64, v_d + ((2 * c * kChunkBytes + ks * 2048) >> 4), p_d + ks * 2, id_v,
+                       ks > 0 || !(flags & kFirst));
+            mma_commit(&ms.empty[st][c]);
+          }
+          mma_commit(&ms.pv_done);
+        }
+      }
+      __syncwarp();
+    }
+    if (elect_one()) mma_commit(&ms.drain);
     __syncwarp();
   } else if (warp < 4) {
     // ================================================================ softmax and output
@@ -564,7 +679,23 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       if (!(flags & (kNull | kEnd))) {
         uint32_t r[32];
         tmem_ld_16x64(tbase + kTmemS + b * 64 + lane_base, r);
-        tmem_ld_wait();
+        float ks[16];  // fp8: the scales of this thread's keys
+        if (FP8) {
+          uint32_t e[32];
+          tmem_ld_16x64(tbase + kTmemPe + b * 64 + lane_base, e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 v = *reinterpret_cast<const float2*>(&ms.scale[i & (kInfo - 1)][8 * j + cq]);
+            ks[2 * j] = v.x;
+            ks[2 * j + 1] = v.y;
+          }
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            r[j] = __float_as_uint(fmaf(__uint_as_float(r[j]), ks[2 * (j >> 2) + (j & 1)], __uint_as_float(e[j])));
+        } else {
+          tmem_ld_wait();
+        }
         tc_fence_before();
         mbar_arrive(&ms.s_empty[b]);
         const unsigned long long mask = f.mask;
@@ -617,7 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
             const float a = ex2(fmaf(__uint_as_float(r[4 * j + 2 * h]), p.scale_log2, neg[h]));
             const float c = ex2(fmaf(__uint_as_float(r[4 * j + 2 * h + 1]), p.scale_log2, neg[h]));
             l[h] += a + c;
-            w[2 * j + h] = pack_bf16(a, c);
+            // fp8: the weight carries the key's scale (an unseen key's scale may be anything)
+            if (FP8 && whole) w[2 * j + h] = pack_bf16(a * ks[2 * j], c * ks[2 * j + 1]);
+            else if (FP8) w[2 * j + h] = pack_bf16(a == 0.f ? 0.f : a * ks[2 * j], c == 0.f ? 0.f : c * ks[2 * j + 1]);
+            else w[2 * j + h] = pack_bf16(a, c);
           }
         }
       } else if (!end && !dead) {
@@ -626,7 +760,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       // the previous value product is done: the weights' buffer is free and the sums hold still
       if (i > 0 && !dead && !warp_wait(&ms.pv_done, (i - 1) & 1, abort_flag, p.status, limit)) dead = true;
       if (bar_red_or(1, kSoftmax, dead || end || grow)) {
-        if (bar_red_or(1, kSoftmax, dead || end)) break;
+        if (bar_red_or(1, kSoftmax, dead || end)) {
+          mbar_arrive(&ms.p_full);  // the value warp sees the end too
+          break;
+        }
         if ((lane & 3) == 0) {
           ms.stat_m[rr] = fac[0];
           ms.stat_m[rr + 8] = fac[1];
@@ -716,9 +853,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       named_bar_sync(2, kSoftmax);  // stat_m and stat_l are read before the next group writes them
     }
   }
+  if (warp == 12) {
+    // every MMA issued has finished before shared memory and TMEM go away
+    const uint64_t td = global_timer_ns();
+    while (!mbar_try_wait(&ms.drain, 0) && global_timer_ns() - td < 200000000ull) {
+    }
+  }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -766,8 +909,8 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_consta
 }
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, cudaStream_t st) {
-  if (fp8) return cudaErrorNotSupported;
-  auto kern = paged ? latent_attn_kernel<true> : latent_attn_kernel<false>;
+  auto kern = paged ? (fp8 ? latent_attn_kernel<true, true> : latent_attn_kernel<true, false>)
+                    : (fp8 ? latent_attn_kernel<false, true> : latent_attn_kernel<false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   const int grid = p.parts * p.ncg;

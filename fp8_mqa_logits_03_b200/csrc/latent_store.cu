@@ -8,7 +8,7 @@
 //   a' = a cos - b sin,  b' = b cos + a sin          (fp32, one rounding to bf16)
 // The latent is stored as it is (bf16 pool), or as e4m3 codes with the
 // indexer pool's rule s = max(max |c|, 1e-4) / 448, codes e4m3(c / s), the
-// scale and the quotient in fp32.
+// scale and the quotient in fp32 (a latent that holds a NaN has the scale NaN).
 //
 // One warp per (token, part): part 0 is the cache entry, part 1 + g the
 // heads [16 g, 16 g + 16).  A vector of 64 values takes four lanes, eight
@@ -44,11 +44,8 @@ __device__ __forceinline__ uint32_t e4m3x4_rn_sat(float a, float b, float c, flo
   return lo | (static_cast<uint32_t>(hi) << 16);
 }
 
-// |x| as ordered bits; NaN counts as 0 (it is left out of a row's maximum).
-__device__ __forceinline__ uint32_t abs_bits_no_nan(float f) {
-  const uint32_t b = __float_as_uint(f) & 0x7FFFFFFFu;
-  return b > 0x7F800000u ? 0u : b;
-}
+// |x| as bits: they order like the values, with NaN above infinity.
+__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
 
 struct Angles {
   float c[8], s[8];
@@ -162,10 +159,11 @@ __global__ void __launch_bounds__(kStoreWarps * 32) latent_store_kernel(const La
       const uint32_t w = (&v[i >> 2].x)[i & 3];
       f[2 * i] = bf_lo(w);
       f[2 * i + 1] = bf_hi(w);
-      m = max(m, max(abs_bits_no_nan(f[2 * i]), abs_bits_no_nan(f[2 * i + 1])));
+      m = max(m, max(abs_bits(f[2 * i]), abs_bits(f[2 * i + 1])));
     }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
-    const float sc = fmaxf(__uint_as_float(m), 1e-4f) / 448.0f;
+    // a latent with a NaN gets the scale NaN, so that attention to it is NaN
+    const float sc = m > 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__uint_as_float(m), 1e-4f) / 448.0f;
     uint4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i)

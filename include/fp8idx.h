@@ -277,7 +277,8 @@ int fp8idx_topk_transform(const int32_t* idx, int64_t rows, int topk, const int3
  *   fp8 pool:  kv_pool [num_slots, 512] e4m3 codes, s_pool [num_slots] fp32,
  *              pe_pool [num_slots, 64] bf16; the codes and the scale follow
  *              fp8idx_act_quant_store's rule over the 512 latent values
- *              (s = max(max |c|, 1e-4) / 448, NaN left out of the maximum)
+ *              (s = max(max |c|, 1e-4) / 448), but a latent that holds a
+ *              NaN gets the scale NaN, so that attention to it gives NaN
  *   q_pe, q_out  [T, H, 64] bf16 with row and head strides in values, H in
  *              [1, 128]; q_out may be q_pe itself, and otherwise must not
  *              overlap it (it is usually the last 64 of the [T, H, 576]
