@@ -22,13 +22,14 @@
 //              four lanes a head), running maximum and sum in registers,
 //              weights as bf16 into shared memory; at a group's end they read
 //              the sums from TMEM, divide and write.
-//   warps 4-11 producers: gather the tile's key rows, one tile ahead, into
-//              registers (16-byte loads), and write them in the 128-byte
-//              swizzle into one of two stages as it comes free; fp8 codes
-//              become bf16 on the way, exactly, and the scales go to the
-//              softmax warps.
-//   warp 12    issues the score products, part by part as a tile lands.
-//   warp 13    issues the value products.
+//   warps 4-7  (fp8: 4-11) producers: gather the tile's key rows into one of
+//              two stages in the 128-byte swizzle.  bf16: 16-byte
+//              asynchronous copies.  fp8: two sets of four warps, each with
+//              every second tile: its codes wait in registers until the stage
+//              is free and become bf16 on the way into it, exactly; the
+//              scales go to the softmax warps.
+//   two more   one issues the score products, part by part as a tile lands,
+//   warps      the other the value products.
 // Scores: M = 64 columns, N = 64 keys, K = 576.  Values, transposed so that
 // the sums of all 512 values fit in half of TMEM: M = 128 values (the same
 // key rows read as an MN-major operand), N = 64 columns, K = 64 keys.
@@ -50,9 +51,9 @@ constexpr int kStageBytes = kChunks * kChunkBytes;
 constexpr int kParts = 5;                       // barriers of a stage: four chunk pairs, and the rotated part
 constexpr int kInfo = 4;                        // tile descriptions in flight
 constexpr int kSoftmax = 128;
-constexpr int kProducers = 256;
-constexpr int kProdWarps = kProducers / 32;
-constexpr int kThreads = kSoftmax + kProducers + 64;
+constexpr int kSet = 128;                       // threads that bring one tile
+__host__ __device__ constexpr int threads_of(bool fp8) { return kSoftmax + (fp8 ? 2 : 1) * kSet + 64; }
+constexpr int kMaxThreads = threads_of(true);
 
 // shared memory, from a 1024-byte boundary
 constexpr int kOffQ = 0;
@@ -90,18 +91,19 @@ struct Misc {
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full, pv_done, drain;
   Info info[kInfo];
-  float scale[kInfo][kAttnKeys];  // fp8: the tile's key scales (0 for a key that does not exist)
+  float scale[2][3][kAttnKeys];  // fp8: the tile's key scales s, log2 s and 1 / s
+  float q_scale[2][kAttnCols];  // fp8: what a column's scores are multiplied by (log2 units)
   float stat_m[kAttnCols], stat_l[kAttnCols];
   uint32_t tmem;
   int abort_flag;
-  int scan[kThreads / 32 + 1];
+  int scan[kMaxThreads / 32];
   int start_group, start_tile;
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc");
 
 // ---------------------------------------------------------------- PTX
 
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -111,9 +113,9 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
-// bf16 x bf16 -> f32; a_mn: A is MN-major (B is K-major).
-__host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+// bf16 x bf16 (or f16 x f16) -> f32; a_mn: A is MN-major (B is K-major).
+__host__ __device__ constexpr uint32_t idesc_16_f32(int M, int N, bool a_mn, bool f16) {
+  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
@@ -186,14 +188,24 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Bytes `2 i` and `2 i + 1` of w as a bf16 pair, exactly: an e4m3 code shifted
-// into bf16's exponent and mantissa is its value times 2^-120 (subnormals
-// included), and the product with 2^120 is exact.
-__device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t w, int i) {
-  const uint32_t t = __byte_perm(w, 0, i == 0 ? 0x1404 : 0x3424);  // codes in the upper bytes of the halves
-  uint32_t v = ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x7B807B80u));
-  return v;
+// The e4m3 codes in the lower and upper half of w as fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four 8 x 8 matrices of 16-bit values, each stored transposed: this lane
+// gives the address of one 16-byte row.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -240,7 +252,9 @@ __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kAttnKey
 // ---------------------------------------------------------------- the kernel
 
 template <bool PAGED, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_constant__ LatentAttnParams p) {
+__global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const __grid_constant__ LatentAttnParams p) {
+  constexpr int kThreads = threads_of(FP8);
+  constexpr int kScoreWarp = kThreads / 32 - 2, kValueWarp = kThreads / 32 - 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -251,10 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s)
       for (int i = 0; i < kParts; ++i) {
-        mbar_init(&ms.full[s][i], kProdWarps);
+        // fp8: one arrival a warp; bf16: one a thread, and one with the tile's description
+        mbar_init(&ms.full[s][i], FP8 ? kSet / 32 : kSet + (i == 0 ? 1 : 0));
         mbar_init(&ms.empty[s][i], 1);
       }
-    mbar_init(&ms.q_full, kProducers);
+    mbar_init(&ms.q_full, kSet);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ms.s_full[b], 1);
       mbar_init(&ms.s_empty[b], kSoftmax);
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     fence_mbar_init();
     p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (warp == 12) {
+  if (warp == kScoreWarp) {
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
@@ -322,10 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   const int64_t x1 = part < parts ? (part + 1) * total / parts : 0;
   const uint32_t tbase = ms.tmem;
 
-  if (warp >= 4 && warp < 12) {
+  if (warp >= 4 && warp < kScoreWarp) {
     // ================================================================ producers
-    const int pt = tid - kSoftmax;
-    const int piece = pt & 7, r0 = pt >> 3;  // 16-byte piece of a chunk row; rows r0 and r0 + 32
+    const int set = (tid - kSoftmax) / kSet, pt = (tid - kSoftmax) % kSet;
+    const int piece = pt & 7, r0 = pt >> 3;  // 16-byte piece of a chunk row; rows r0 + 16 k
     const uint32_t row_dst = smem_u32(smem + kOffK) + r0 * 128;
     const uint32_t swz = (piece ^ (r0 & 7)) << 4;
     // fp8: 16 codes become pieces 2 (piece % 4) and the next of chunk piece / 4;
@@ -359,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       direct = t == 0 && te == nt;
       slot = blockIdx.x * 2 + (t == 0 ? 1 : 0);
       fresh = true;
-      if (t == 0 && te < nt && pt == 0) {
+      if (t == 0 && te < nt && set == 0 && pt == 0) {
         // the group goes on in the ranges after this one, up to the one that holds its last tile
         const int64_t last = x + nt - 1;
         const int c1 = static_cast<int>(((last + 1) * parts - 1) / total);
@@ -381,13 +396,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       }
     };
 
-    // ---- the tile about to be written, its rows on the way in registers
+    // ---- the tile about to be written (fp8: its rows on the way in registers)
     Info d;
-    uint4 raw[FP8 ? 10 : 18];
+    uint4 raw[FP8 ? 20 : 1];
     float sc = 0.f;
-    const uint8_t* src[2];
-    const uint8_t* pe_src[2];
-    bool have[2];
+    const uint8_t* src[4];
+    const uint8_t* pe_src[4];
+    bool have[4];
     // Finds the next tile that holds keys (or ends a segment, or the stream) and describes it in d.
     auto advance = [&]() {
       for (;;) {
@@ -433,51 +448,47 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         if (!null) {
           fresh = false;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int64_t v = __shfl_sync(0xFFFFFFFFu, sl[k], r0);
+          for (int k = 0; k < 4; ++k) {
+            const int64_t v = __shfl_sync(0xFFFFFFFFu, sl[k >> 1], (r0 + 16 * k) & 31);
             have[k] = v >= 0;
             src[k] = p.kv + (v >= 0 ? v : 0) * kRowBytes + piece * 16;
             if (FP8) pe_src[k] = p.pe + (v >= 0 ? v : 0) * (kRope * 2) + piece * 16;
           }
           if (FP8 && pt < kAttnKeys) {
             const int64_t v = pt < 32 ? sl[0] : sl[1];
-            sc = v >= 0 ? __ldg(p.s + v) : 0.f;
+            // a scale of 0 (or below 2^-60) counts as 2^-60: its log and inverse are used
+            const float x = v >= 0 ? __ldg(p.s + v) : 1.f;
+            sc = x < 8.673617379884035e-19f ? 8.673617379884035e-19f : x;
           }
         }
         return;
       }
     };
-    // Loads of part c (0-3: two chunks; 4: the rotated part) into its registers.
-    auto load_part = [&](int c) {
+    // fp8: the tile's codes (16 bytes of part c in raw[4 c + k]) and rotated rows.
+    auto load_raw = [&]() {
+      if (FP8) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (FP8) {
-          raw[2 * c + k] = have[k] ? ld_stream16(c < 4 ? src[k] + c * 128 : pe_src[k]) : make_uint4(0, 0, 0, 0);
-        } else {
+        for (int c = 0; c < kParts; ++c)
 #pragma unroll
-          for (int u = 0; u < (c < 4 ? 2 : 1); ++u)
-            raw[4 * c + 2 * u + k] = have[k] ? ld_stream16(src[k] + (2 * c + u) * 128) : make_uint4(0, 0, 0, 0);
-        }
+          for (int k = 0; k < 4; ++k)
+            raw[4 * c + k] = have[k] ? ld_stream16(c < 4 ? src[k] + c * 128 : pe_src[k]) : make_uint4(0, 0, 0, 0);
       }
     };
     auto store_part = [&](int c, uint32_t dst) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t rd = dst + k * 4096 + 2 * c * kChunkBytes;
-        if (FP8 && c < 4) {
-          const uint4 v = raw[2 * c + k];
-          const uint32_t a[4] = {e4m3_pair_bf16(v.x, 0), e4m3_pair_bf16(v.x, 1), e4m3_pair_bf16(v.y, 0),
-                                 e4m3_pair_bf16(v.y, 1)};
-          const uint32_t b[4] = {e4m3_pair_bf16(v.z, 0), e4m3_pair_bf16(v.z, 1), e4m3_pair_bf16(v.w, 0),
-                                 e4m3_pair_bf16(v.w, 1)};
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t rd = dst + k * 2048 + 2 * c * kChunkBytes;
+        const uint4 v = raw[FP8 ? 4 * c + k : 0];
+        if (c < 4) {
+          uint32_t a[4], b[4];
+          e4m3x4_f16(v.x, a[0], a[1]);
+          e4m3x4_f16(v.y, a[2], a[3]);
+          e4m3x4_f16(v.z, b[0], b[1]);
+          e4m3x4_f16(v.w, b[2], b[3]);
           st_shared16(rd + fdst0, odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? b[2] : a[2], odd ? b[3] : a[3]);
           st_shared16(rd + fdst1, odd ? a[0] : b[0], odd ? a[1] : b[1], odd ? a[2] : b[2], odd ? a[3] : b[3]);
         } else {
-#pragma unroll
-          for (int u = 0; u < (c < 4 ? 2 : 1); ++u) {
-            const uint4 v = raw[FP8 ? 2 * c + k : 4 * c + 2 * u + k];
-            st_shared16(rd + u * kChunkBytes + swz, v.x, v.y, v.z, v.w);
-          }
+          st_shared16(rd + swz, v.x, v.y, v.z, v.w);
         }
       }
     };
@@ -490,83 +501,136 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       t = te;
     }
     advance();
-    if (!(d.flags & (kNull | kEnd))) {
-#pragma unroll
-      for (int c = 0; c < kParts; ++c) load_part(c);
-    }
-    for (int i = 0;; ++i) {
+    if (set == 1 && !(d.flags & kEnd)) advance();
+    else if (set == 1) ok = false;  // set 0 announces the end
+    if (FP8 && ok && !(d.flags & (kNull | kEnd))) load_raw();
+    for (int i = set; ok; i += FP8 ? 2 : 1) {
       const int st = i & 1;
       const uint32_t ph = (i >> 1) & 1;
       const int flags = d.flags;
       const bool null = flags & (kNull | kEnd);
+      float qfac[4];
       if ((flags & kFirst) && !null) {
-        // ---- the group's query columns; their place is free once the last tile's scores are done
-        if (i > 0 && !warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, p.status, limit)) {
-          ok = false;
-          break;
-        }
+        // ---- the group's query columns; their place is free once the scores
+        // of tile i - 1 are done.  Tile i - 2's first: only then is the other
+        // barrier's phase the one asked for or the one before it (a set sees
+        // every second tile alone).
+        if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, p.status, limit)) break;
+        if (i > 0 && !warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, p.status, limit)) break;
         const int cols = p.R * p.H;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int col = cg * kAttnCols + r0 + 32 * k;
+        for (int k = 0; k < 4; ++k) {
+          const int col = cg * kAttnCols + r0 + 16 * k;
           const bool v = col < cols;
           const int row = v ? col / p.H : 0, h = v ? col - row * p.H : 0;
           const uint8_t* qs = reinterpret_cast<const uint8_t*>(
-              p.q + (static_cast<int64_t>(d.group) * p.R + row) * p.q_row + h * p.q_head);
-          const uint32_t qd = smem_u32(smem + kOffQ) + (r0 + 32 * k) * 128 + swz;
+              p.q + (static_cast<int64_t>(d.group) * p.R + row) * p.q_row + h * p.q_head) + piece * 16;
+          const uint32_t qd = smem_u32(smem + kOffQ) + (r0 + 16 * k) * 128 + swz;
+          if (!FP8) {
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            cp_async16(qd + c * kChunkBytes, qs + c * 128 + piece * 16, v ? 16 : 0);
+            for (int c = 0; c < kChunks; ++c) cp_async16(qd + c * kChunkBytes, qs + c * 128, v ? 16 : 0);
+          } else {
+            // The codes are products' other side in fp16, so a column becomes
+            // fp16 too, times the power of two that brings its largest value
+            // next to 2^14: exact but for values 2^28 times smaller, whose
+            // error (2^-39 of the largest) is below the fp32 sum's.
+            uint32_t m = 0;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const uint4 x = v ? __ldg(reinterpret_cast<const uint4*>(qs + c * 128)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t y = (&x.x)[e] & 0x7FFF7FFFu;
+                m = max(m, max(y & 0xFFFFu, y >> 16));
+              }
+            }
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+            const int ex = m >> 7;  // biased exponent of the largest value
+            // times 2^(140 - ex), as two factors that are ordinary numbers; a zero or non-finite column stays
+            const int up = ex == 0 || ex == 255 ? 0 : 140 - ex, up0 = up / 2, up1 = up - up0;
+            const float f0 = __uint_as_float(static_cast<uint32_t>(127 + up0) << 23);
+            const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up1) << 23);
+            qfac[k] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up0) << 23) *
+                      __uint_as_float(static_cast<uint32_t>(127 - up1) << 23);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const uint4 x = v ? __ldg(reinterpret_cast<const uint4*>(qs + c * 128)) : make_uint4(0, 0, 0, 0);
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t y = (&x.x)[e];
+                const float lo = __uint_as_float(y << 16) * f0 * f1, hi = __uint_as_float(y & 0xFFFF0000u) * f0 * f1;
+                o[e] = c < 8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);  // the rotated part meets bf16
+              }
+              st_shared16(qd + c * kChunkBytes, o[0], o[1], o[2], o[3]);
+            }
+          }
         }
-        cp_async_arrive(&ms.q_full);
+        if (FP8) {
+          fence_async_shared();
+          mbar_arrive(&ms.q_full);
+        } else {
+          cp_async_arrive(&ms.q_full);
+        }
       }
       // ---- describe the tile.  The entry was tile i - 4's; the values of
       // tile i - 2 have begun, so every role is past tile i - 4.
-      if (!warp_wait(&ms.empty[st][0], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
-      if (pt == 0) ms.info[i & (kInfo - 1)] = d;
-      if (FP8 && pt < kAttnKeys) ms.scale[i & (kInfo - 1)][pt] = sc;
-      const bool withhold = p.debug_withhold_first_tile && i == 0;
-      if (null) {
-#pragma unroll 1
-        for (int c = 0; c < kParts; ++c) {
-          if (c > 0 && !(flags & kEnd) && !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) {
-            ok = false;
-            break;
-          }
-          __syncwarp();
-          if (lane == 0 && !withhold) mbar_arrive(&ms.full[st][c]);
-        }
-        if (!ok || (flags & kEnd)) break;
-        advance();
-        if (!(d.flags & (kNull | kEnd))) {
-#pragma unroll
-          for (int c = 0; c < kParts; ++c) load_part(c);
-        }
-        continue;
+      if (!warp_wait(&ms.empty[st][0], ph ^ 1, abort_flag, p.status, limit)) break;
+      if (pt == 0) {
+        ms.info[i & (kInfo - 1)] = d;
+        if (!FP8) mbar_arrive(&ms.full[st][0]);
       }
-      // ---- write it part by part, and put the next tile's loads in flight behind each
-      advance();
-      const bool more = !(d.flags & (kNull | kEnd));
+      if (FP8 && pt < kAttnKeys) {
+        ms.scale[st][0][pt] = sc;
+        ms.scale[st][1][pt] = log2f(sc);
+        ms.scale[st][2][pt] = 1.f / sc;
+      }
+      if (FP8 && (flags & kFirst) && !null && piece == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ms.q_scale[st][r0 + 16 * k] = qfac[k];
+      }
+      const bool withhold = p.debug_withhold_first_tile && i == 0;
       const uint32_t dst = row_dst + st * kStageBytes;
 #pragma unroll
       for (int c = 0; c < kParts; ++c) {
+        if (c > 0 && (flags & kEnd)) break;
         if (c > 0 && !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
-        store_part(c, dst);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0 && !(withhold && c == 0)) mbar_arrive(&ms.full[st][c]);
-        if (more) load_part(c);
+        if (FP8) {
+          if (!null) store_part(c, dst);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0 && !(withhold && c == 0)) mbar_arrive(&ms.full[st][c]);
+        } else if (null) {
+          mbar_arrive(&ms.full[st][c]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < (c < 4 ? 2 : 1); ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              cp_async16(dst + (2 * c + u) * kChunkBytes + k * 2048 + swz, src[k] + (2 * c + u) * 128,
+                         have[k] ? 16 : 0);
+          if (!(withhold && c == 0)) cp_async_arrive(&ms.full[st][c]);
+        }
       }
-      if (!ok) break;
+      if (flags & kEnd) break;
+      // ---- the next tile (fp8: of this set; its loads go out now, with no fence behind them until they are used)
+      advance();
+      if (FP8) {
+        if (d.flags & kEnd) break;  // the other set announces it
+        advance();
+        if (!(d.flags & (kNull | kEnd))) load_raw();
+      }
     }
     cp_async_wait_all();
     if (bad && cg == 0) atomicOr(p.status, bad);
-  } else if (warp == 12) {
+  } else if (warp == kScoreWarp) {
     // ================================================================ score products
     // A whole warp runs the issue loops, so that descriptors and branches are
     // uniform, and one elected lane issues: MMAs issued from a branch on the
     // lane number took 280 cycles each, elected ones 32 (scores) and 49.
-    constexpr uint32_t id_s = idesc_bf16_f32(64, 64, false);
+    constexpr uint32_t id_s = idesc_16_f32(64, 64, false, FP8), id_pe = idesc_16_f32(64, 64, false, false);
     const uint64_t q_d = smem_desc_k128_sw128(smem_u32(smem + kOffQ));
     int nq = 0;  // query loads seen
     for (int i = 0;; ++i) {
@@ -592,19 +656,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       if (flags & kFirst) {
         if (!warp_wait(&ms.q_full, nq & 1, abort_flag, p.status, limit)) break;
         ++nq;
-        fence_async_shared();  // the queries came by asynchronous copies of other threads
+        if (!FP8) fence_async_shared();  // the queries came by asynchronous copies of other threads
       }
       bool ok = true;
 #pragma unroll
       for (int c = 0; c < kParts; ++c) {
         if (c > 0 && !warp_wait(&ms.full[st][c], ph, abort_flag, p.status, limit)) { ok = false; break; }
+        if (!FP8) fence_async_shared();  // the rows came by asynchronous copies of other threads
         tc_fence_after();
         if (elect_one()) {
           const uint32_t dd = tbase + (FP8 && c == 4 ? kTmemPe : kTmemS) + st * 64;
 #pragma unroll
           for (int ks = 0; ks < (c < 4 ? 8 : 4); ++ks) {
             const int off = ((2 * c + (ks >> 2)) * kChunkBytes + (ks & 3) * 32) >> 4;
-            mma_bf16(dd, q_d + off, k_d + off, id_s, ks > 0 || (c > 0 && !(FP8 && c == 4)));
+            mma_16(dd, q_d + off, k_d + off, c == 4 ? id_pe : id_s, ks > 0 || (c > 0 && !(FP8 && c == 4)));
           }
           if (c == 4) {
             mma_commit(&ms.empty[st][4]);
@@ -617,9 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     }
     if (elect_one()) mma_commit(&ms.drain);
     __syncwarp();
-  } else if (warp == 13) {
+  } else if (warp == kValueWarp) {
     // ================================================================ value products
-    constexpr uint32_t id_v = idesc_bf16_f32(128, 64, true);
+    constexpr uint32_t id_v = idesc_16_f32(128, 64, true, FP8);
     const uint64_t p_d = smem_desc_k128_sw128(smem_u32(smem + kOffP));
     for (int i = 0;; ++i) {
       const int st = i & 1;
@@ -638,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
           for (int c = 0; c < 4; ++c) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_bf16(tbase + kTmemO + c * 64, v_d + ((2 * c * kChunkBytes + ks * 2048) >> 4), p_d + ks * 2, id_v,
+              mma_16(tbase + kTmemO + c * 64, v_d + ((2 * c * kChunkBytes + ks * 2048) >> 4), p_d + ks * 2, id_v,
                        ks > 0 || !(flags & kFirst));
             mma_commit(&ms.empty[st][c]);
           }
@@ -658,8 +723,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     int trow[2];                             // row within the group of each column
 #pragma unroll
     for (int h = 0; h < 2; ++h) trow[h] = PAGED ? min((cg * kAttnCols + rr + 8 * h) / p.H, p.R - 1) : 0;
+    // fp8: weights are fp16, whose range the maximum is moved away from the
+    // lower end of (2^7 next to it, 2^15 before a rescale; 2^-24 is the smallest)
+    constexpr float kBias = FP8 ? 7.f : 0.f;
     uint8_t* prow = smem + kOffP + rr * 128 + 2 * cq;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float to_log2[2] = {p.scale_log2, p.scale_log2};
     for (int i = 0;; ++i) {
       const int b = i & 1;
       // a wait that gave up is carried to the votes below, so that all four
@@ -672,6 +741,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       if (flags & kFirst) {
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
+        if (FP8) {
+          to_log2[0] = ms.q_scale[b][rr];
+          to_log2[1] = ms.q_scale[b][rr + 8];
+        }
       }
       uint32_t w[16];
       float fac[2] = {1.f, 1.f};
@@ -679,20 +752,25 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       if (!(flags & (kNull | kEnd))) {
         uint32_t r[32];
         tmem_ld_16x64(tbase + kTmemS + b * 64 + lane_base, r);
-        float ks[16];  // fp8: the scales of this thread's keys
         if (FP8) {
           uint32_t e[32];
           tmem_ld_16x64(tbase + kTmemPe + b * 64 + lane_base, e);
+          tmem_ld_wait();
+          // (codes . q) s + rotated part, in log2 units, plus log2 s: the
+          // weight of key j is exp2 of this, i.e. it carries the key's scale
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float2 v = *reinterpret_cast<const float2*>(&ms.scale[i & (kInfo - 1)][8 * j + cq]);
-            ks[2 * j] = v.x;
-            ks[2 * j + 1] = v.y;
-          }
-          tmem_ld_wait();
+            const float2 v = *reinterpret_cast<const float2*>(&ms.scale[b][0][8 * j + cq]);
+            const float2 g = *reinterpret_cast<const float2*>(&ms.scale[b][1][8 * j + cq]);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            r[j] = __float_as_uint(fmaf(__uint_as_float(r[j]), ks[2 * (j >> 2) + (j & 1)], __uint_as_float(e[j])));
+            for (int h = 0; h < 2; ++h) {
+              const int x = 4 * j + 2 * h;
+              r[x] = __float_as_uint(
+                  fmaf(fmaf(__uint_as_float(r[x]), v.x, __uint_as_float(e[x])), to_log2[h], g.x));
+              r[x + 1] = __float_as_uint(
+                  fmaf(fmaf(__uint_as_float(r[x + 1]), v.y, __uint_as_float(e[x + 1])), to_log2[h], g.y));
+            }
+          }
         } else {
           tmem_ld_wait();
         }
@@ -730,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         for (int h = 0; h < 2; ++h) {
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
-          mx[h] *= p.scale_log2;
+          mx[h] = (FP8 ? mx[h] : mx[h] * to_log2[h]) - kBias;
           if (flags & kFirst) {
             m[h] = mx[h];
           } else if (mx[h] > m[h] + kRescaleLog2) {
@@ -743,15 +821,22 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+          float2 inv;
+          if (FP8) inv = *reinterpret_cast<const float2*>(&ms.scale[b][2][8 * j + cq]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float a = ex2(fmaf(__uint_as_float(r[4 * j + 2 * h]), p.scale_log2, neg[h]));
-            const float c = ex2(fmaf(__uint_as_float(r[4 * j + 2 * h + 1]), p.scale_log2, neg[h]));
-            l[h] += a + c;
-            // fp8: the weight carries the key's scale (an unseen key's scale may be anything)
-            if (FP8 && whole) w[2 * j + h] = pack_bf16(a * ks[2 * j], c * ks[2 * j + 1]);
-            else if (FP8) w[2 * j + h] = pack_bf16(a == 0.f ? 0.f : a * ks[2 * j], c == 0.f ? 0.f : c * ks[2 * j + 1]);
-            else w[2 * j + h] = pack_bf16(a, c);
+            const float x = __uint_as_float(r[4 * j + 2 * h]), y = __uint_as_float(r[4 * j + 2 * h + 1]);
+            if (FP8) {
+              const float a = ex2(x + neg[h]), c = ex2(y + neg[h]);
+              // (an unseen key's scale may be anything)
+              l[h] = a == 0.f ? l[h] : fmaf(a, inv.x, l[h]);
+              l[h] = c == 0.f ? l[h] : fmaf(c, inv.y, l[h]);
+              w[2 * j + h] = pack_f16(a, c);
+            } else {
+              const float a = ex2(fmaf(x, to_log2[h], neg[h])), c = ex2(fmaf(y, to_log2[h], neg[h]));
+              l[h] += a + c;
+              w[2 * j + h] = pack_bf16(a, c);
+            }
           }
         }
       } else if (!end && !dead) {
@@ -824,36 +909,74 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         ms.stat_l[tid] = ll == 0.f ? 0.f : 1.f / ll;
       }
       named_bar_sync(2, kSoftmax);
-      float* po = p.part_o + (static_cast<int64_t>(slot) * kAttnCols) * kLatent + warp * 32 + lane;
-      uint16_t* oo = p.out + col0 * kLatent + warp * 32 + lane;
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) {  // 128 values c / 2, columns 32 (c % 2) + k
-        if ((c & 1) * 32 >= n) continue;
-        uint32_t o[32];
-        if (none) {
+      if (direct) {
+        // 16 values x 64 columns at a time: divided, rounded, transposed
+        // through the warp's quarter of the weights' buffer, and written as
+        // 16-byte pieces (8 values of one column)
+        float inv[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
-        } else {
-          tmem_ld32(tbase + kTmemO + c * 32 + lane_base, o);
-          tmem_ld_wait();
+        for (int j = 0; j < 8; ++j) {
+          const float2 v = *reinterpret_cast<const float2*>(&ms.stat_l[8 * j + cq]);
+          inv[2 * j] = v.x;
+          inv[2 * j + 1] = v.y;
         }
+        uint8_t* tb = smem + kOffP + warp * 2048;
+        const int mrow = (lane >> 4) * 8 + (lane & 7);  // stmatrix: this lane's column (of 16) and value half
+        const uint32_t maddr = smem_u32(tb) + mrow * 32 + ((((lane >> 3) & 1) ^ ((mrow >> 2) & 1)) << 4);
+        uint16_t* oo = p.out + col0 * kLatent + warp * 32;
+#pragma unroll 2
+        for (int c = 0; c < 8; ++c) {  // values 128 (c / 2) + 32 warp + 16 (c % 2) + {0 .. 15}
+          uint32_t o[32];
+          if (none) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int col = (c & 1) * 32 + k;
-          if (col >= n) break;
-          const float v = __uint_as_float(o[k]);
-          if (direct)
-            oo[static_cast<int64_t>(col) * kLatent + (c >> 1) * 128] =
-                static_cast<uint16_t>(pack_bf16(v * ms.stat_l[col], 0.f));
-          else
-            po[static_cast<int64_t>(col) * kLatent + (c >> 1) * 128] = v;
+            for (int k = 0; k < 32; ++k) o[k] = 0;
+          } else {
+            tmem_ld_16x64(tbase + kTmemO + (c >> 1) * 64 + lane_base + (static_cast<uint32_t>(c & 1) << 20), o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            o[2 * j] = pack_bf16(__uint_as_float(o[4 * j]) * inv[2 * j], __uint_as_float(o[4 * j + 1]) * inv[2 * j + 1]);
+            o[2 * j + 1] =
+                pack_bf16(__uint_as_float(o[4 * j + 2]) * inv[2 * j], __uint_as_float(o[4 * j + 3]) * inv[2 * j + 1]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) stmatrix_x4_trans(maddr + j * 512, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int col = k * 16 + (lane >> 1), half = lane & 1;
+            const uint4 v = *reinterpret_cast<const uint4*>(tb + col * 32 + ((half ^ ((col >> 2) & 1)) << 4));
+            if (col < n)
+              *reinterpret_cast<uint4*>(oo + static_cast<int64_t>(col) * kLatent + (c >> 1) * 128 + (c & 1) * 16 + half * 8) = v;
+          }
+        }
+      } else {
+        // [slot][value block, column half][column quad][value][column of the quad]
+        float* po = p.part_o + (static_cast<int64_t>(slot) * 64 * 128 + tid) * 4;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          if ((c & 1) * 32 >= n) continue;
+          uint32_t o[32];
+          if (none) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0;
+          } else {
+            tmem_ld32(tbase + kTmemO + c * 32 + lane_base, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if ((c & 1) * 32 + 4 * j < n)
+              *reinterpret_cast<uint4*>(po + (c * 8 + j) * 512) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
       }
       tc_fence_before();
       named_bar_sync(2, kSoftmax);  // stat_m and stat_l are read before the next group writes them
     }
   }
-  if (warp == 12) {
+  if (warp == kScoreWarp) {
     // every MMA issued has finished before shared memory and TMEM go away
     const uint64_t td = global_timer_ns();
     while (!mbar_try_wait(&ms.drain, 0) && global_timer_ns() - td < 200000000ull) {
@@ -861,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -869,43 +992,59 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
 
 // ---------------------------------------------------------------- joining cut groups
 
-// Block (x, y): the group whose first piece CTA x holds, columns [8 y, 8 y + 8).
-// The pieces lie in the CTAs x, x + ncg, ..., in key order: the first in its
-// second slot, the others in their first.  128 threads take four values each.
-constexpr int kJoinCols = 8;
-
+// Block (x, y): the group whose first piece CTA x holds, value block y / 16,
+// columns [4 (y % 16), + 4).  The pieces lie in the CTAs x, x + ncg, ..., in
+// key order: the first in its second slot, the others in their first.
 __global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_constant__ LatentAttnParams p) {
+  __shared__ float4 wt[kAttnMaxParts];
   griddep_wait();
   const int4 mt = p.meta[blockIdx.x];
   if (mt.y < 2) return;
   const int cols = p.R * p.H, cg = blockIdx.x % p.ncg;
   const int n = min(kAttnCols, cols - cg * kAttnCols);
-  for (int col = blockIdx.y * kJoinCols; col < min(n, static_cast<int>(blockIdx.y + 1) * kJoinCols); ++col) {
+  const int quad = blockIdx.y & 15, vb = blockIdx.y >> 4;
+  if (4 * quad >= n) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t oc = static_cast<int64_t>(mt.x) * cols + cg * kAttnCols + 4 * quad;
+  auto slot_at = [&](int k) { return static_cast<int64_t>(blockIdx.x + k * p.ncg) * 2 + (k == 0 ? 1 : 0); };
+  {
+    // warp w: the weights of column 4 quad + w in every piece
+    const int col = 4 * quad + warp;
     float top = -INFINITY;
-    for (int k = 0; k < mt.y; ++k) {
-      const int64_t slot = static_cast<int64_t>(blockIdx.x + k * p.ncg) * 2 + (k == 0 ? 1 : 0);
-      top = fmaxf(top, __ldg(&p.part_ml[slot * kAttnCols + col].x));
-    }
+    if (col < n)
+      for (int k = lane; k < mt.y; k += 32) top = fmaxf(top, p.part_ml[slot_at(k) * kAttnCols + col].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     const float ref = top == -INFINITY ? 0.f : top;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    for (int k = 0; k < mt.y; ++k) {
-      const int64_t slot = static_cast<int64_t>(blockIdx.x + k * p.ncg) * 2 + (k == 0 ? 1 : 0);
-      const float2 ml = __ldg(&p.part_ml[slot * kAttnCols + col]);
-      const float w = exp2f(ml.x - ref);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p.part_o + (slot * kAttnCols + col) * kLatent) + threadIdx.x);
-      sum = fmaf(ml.y, w, sum);
-      acc.x = fmaf(v.x, w, acc.x);
-      acc.y = fmaf(v.y, w, acc.y);
-      acc.z = fmaf(v.z, w, acc.z);
-      acc.w = fmaf(v.w, w, acc.w);
-    }
+    if (col < n)
+      for (int k = lane; k < mt.y; k += 32) {
+        const float2 ml = p.part_ml[slot_at(k) * kAttnCols + col];
+        sum = fmaf(ml.y, exp2f(ml.x - ref), sum);
+      }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t oc = static_cast<int64_t>(mt.x) * cols + cg * kAttnCols + col;
-    reinterpret_cast<uint2*>(p.out + oc * kLatent)[threadIdx.x] =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (threadIdx.x == 0 && p.lse) p.lse[oc] = (top + log2f(sum)) * 0.69314718055994531f;
+    for (int k = lane; k < mt.y; k += 32)
+      (&wt[k].x)[warp] = col < n ? exp2f(p.part_ml[slot_at(k) * kAttnCols + col].x - ref) * inv : 0.f;
+    if (vb == 0 && lane == 0 && p.lse && col < n) p.lse[oc + warp] = (top + log2f(sum)) * 0.69314718055994531f;
   }
+  __syncthreads();
+  const float* src = p.part_o + ((vb * 2 + (quad >> 3)) * 8 + (quad & 7)) * 512 + tid * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < mt.y; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(src + slot_at(k) * (kAttnCols * kLatent));
+    const float4 w = wt[k];
+    acc.x = fmaf(v.x, w.x, acc.x);
+    acc.y = fmaf(v.y, w.y, acc.y);
+    acc.z = fmaf(v.z, w.z, acc.z);
+    acc.w = fmaf(v.w, w.w, acc.w);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (4 * quad + e < n)
+      p.out[(oc + e) * kLatent + vb * 128 + tid] = static_cast<uint16_t>(pack_bf16((&acc.x)[e], 0.f));
 }
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, cudaStream_t st) {
@@ -914,11 +1053,11 @@ cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, 
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   const int grid = p.parts * p.ncg;
-  kern<<<grid, kThreads, kSmemBytes, st>>>(p);
+  kern<<<grid, threads_of(fp8), kSmemBytes, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), kAttnCols / kJoinCols);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 64);  // four value blocks x 16 column quads
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -14,6 +14,7 @@ constexpr int kLatentDim = kLatent + kRope;  // key width
 constexpr int kAttnKeys = 64;                // keys per tile (one page)
 constexpr int kAttnCols = 64;                // (row, head) columns of a unit
 constexpr int kAttnMaxHeads = 128;
+constexpr int kAttnMaxParts = 256;            // ranges of the tile axis
 constexpr int kStatusBadSlot = 16;           // device status bit: a selected slot past the pool
 
 struct LatentStoreParams {
@@ -60,7 +61,7 @@ struct LatentAttnParams {
   // CTA x takes column block x % ncg of range x / ncg
   int ncg, parts;
   int* status;
-  float* part_o;            // [grid][2][64][512] unnormalised sums of cut groups
+  float* part_o;            // [grid][2][64 x 512] unnormalised sums of cut groups
   float2* part_ml;          // [grid][2][64] (reference maximum in log2 units, sum)
   int4* meta;               // [grid] (group, pieces, -, -) of the cut group whose first piece the CTA holds
   unsigned long long wait_limit_ns;

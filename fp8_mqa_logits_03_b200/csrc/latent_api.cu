@@ -30,7 +30,7 @@ AttnPlan plan_attn(int64_t groups, int64_t cols, int64_t max_tiles_per_group, in
   AttnPlan pl;
   pl.ncg = static_cast<int>(ceil_div(cols, kAttnCols));
   const int64_t tiles = std::max<int64_t>(1, groups * std::max<int64_t>(1, max_tiles_per_group));
-  pl.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / pl.ncg, tiles)));
+  pl.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / pl.ncg, tiles, kAttnMaxParts})));
   const int64_t grid = static_cast<int64_t>(pl.parts) * pl.ncg;
   int64_t off = kStatusBytes;
   pl.off_meta = off;
