@@ -50,10 +50,21 @@ constexpr int kChunkBytes = kAttnKeys * 128;    // [64 keys][64 values] bf16, sw
 constexpr int kStageBytes = kChunks * kChunkBytes;
 constexpr int kParts = 5;                       // barriers of a stage: four chunk pairs, and the rotated part
 constexpr int kInfo = 4;                        // tile descriptions in flight
-constexpr int kSoftmax = 128;
 constexpr int kSet = 128;                       // threads that bring one tile
-__host__ __device__ constexpr int threads_of(bool fp8) { return kSoftmax + (fp8 ? 2 : 1) * kSet + 64; }
-constexpr int kMaxThreads = threads_of(true);
+
+// The kernel's shape for a kind of pool.
+template <bool FP8>
+struct Shape {
+  static constexpr int kSwg = FP8 ? 1 : 2;        // softmax warpgroups, each with 64 / kSwg of a tile's keys
+  static constexpr int kSoftmax = 128 * kSwg;
+  static constexpr int kSets = FP8 ? 2 : 1;       // producer sets
+  static constexpr int kThreads = kSoftmax + kSets * kSet + 64;
+  static constexpr int kFull = FP8 ? 5 : 2;       // announcements of a tile's parts
+  // the parts that announcement f covers
+  __host__ __device__ static constexpr int first_part(int f) { return FP8 ? f : (f == 0 ? 0 : f == 1 ? 2 : 5); }
+};
+constexpr int kMaxThreads = 448;
+static_assert(Shape<true>::kThreads <= kMaxThreads && Shape<false>::kThreads <= kMaxThreads, "threads");
 
 // shared memory, from a 1024-byte boundary
 constexpr int kOffQ = 0;
@@ -91,8 +102,16 @@ struct Misc {
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full, pv_done, drain;
   Info info[kInfo];
-  float scale[2][3][kAttnKeys];  // fp8: the tile's key scales s, log2 s and 1 / s
-  float q_scale[2][kAttnCols];  // fp8: what a column's scores are multiplied by (log2 units)
+  union {
+    struct {
+      float scale[2][3][kAttnKeys];  // fp8: the tile's key scales s, log2 s and 1 / s, by tile parity
+      float q_scale[2][kAttnCols];   // fp8: what a column's scores are multiplied by (log2 units)
+    };
+    struct {
+      float half_max[2][2][kAttnCols];  // two softmax warpgroups: their keys' maxima, by tile parity
+      float stat_l1[kAttnCols];         // and the second one's sums
+    };
+  };
   float stat_m[kAttnCols], stat_l[kAttnCols];
   uint32_t tmem;
   int abort_flag;
@@ -132,10 +151,10 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
-// 16 lanes x 64 columns: thread t receives, for each 8-column block j, columns
+// 16 lanes x 64 (or 32) columns: thread t receives, for each 8-column block j, columns
 // 8j + 2(t % 4) + {0, 1} of lane t / 4 in r[4j], r[4j+1] and of lane t / 4 + 8
 // in r[4j+2], r[4j+3].
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -145,6 +164,16 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
         "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
@@ -219,7 +248,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// wait_phase by a whole warp; true only where every lane's wait succeeded.
+// A bounded wait by a whole warp; true only where every lane's wait
+// succeeded.  (Polling without suspending was slower: the warps that wait
+// took the shared-memory pipe from those that work.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
                                           unsigned long long limit_ns) {
   return __all_sync(0xFFFFFFFFu, wait_phase<kSpin>(bar, parity, abort_flag, status, limit_ns));
@@ -252,8 +283,9 @@ __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kAttnKey
 // ---------------------------------------------------------------- the kernel
 
 template <bool PAGED, bool FP8>
-__global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const __grid_constant__ LatentAttnParams p) {
-  constexpr int kThreads = threads_of(FP8);
+__global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(const __grid_constant__ LatentAttnParams p) {
+  using Sh = Shape<FP8>;
+  constexpr int kThreads = Sh::kThreads, kSoftmax = Sh::kSoftmax, kSwg = Sh::kSwg;
   constexpr int kScoreWarp = kThreads / 32 - 2, kValueWarp = kThreads / 32 - 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
@@ -265,8 +297,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s)
       for (int i = 0; i < kParts; ++i) {
-        // fp8: one arrival a warp; bf16: one a thread, and one with the tile's description
-        mbar_init(&ms.full[s][i], FP8 ? kSet / 32 : kSet + (i == 0 ? 1 : 0));
+        // codes: one arrival a warp; asynchronous copies: one a thread (bf16: and one with the tile's description)
+        mbar_init(&ms.full[s][i], FP8 && i < 4 ? kSet / 32 : kSet + (i == 0 ? 1 : 0));
         mbar_init(&ms.empty[s][i], 1);
       }
     mbar_init(&ms.q_full, kSet);
@@ -337,7 +369,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
   const int64_t x1 = part < parts ? (part + 1) * total / parts : 0;
   const uint32_t tbase = ms.tmem;
 
-  if (warp >= 4 && warp < kScoreWarp) {
+  if (warp >= kSoftmax / 32 && warp < kScoreWarp) {
     // ================================================================ producers
     const int set = (tid - kSoftmax) / kSet, pt = (tid - kSoftmax) % kSet;
     const int piece = pt & 7, r0 = pt >> 3;  // 16-byte piece of a chunk row; rows r0 + 16 k
@@ -352,12 +384,14 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
     constexpr int kRowBytes = FP8 ? kLatent : kLatentDim * 2;
 
     // ---- where the stream stands: the next tile to look at is tile t of group g
-    int g, t, te = 0, len = 0, slot = 0;
-    bool direct = false, fresh = true;  // fresh: no tile of the segment has been emitted
-    int64_t x = x0;                     // end of the current segment on the tile axis
+    int g, t, te = 0, len = 0;
+    bool direct = false, from_start = false, fresh = true;  // fresh: no tile of the segment has been emitted
+    int left = static_cast<int>(x1 - x0);  // tiles of this CTA's range behind the current segment
     const int32_t* list = nullptr;
     int bad = 0;
-    int next_idx[2] = {-1, -1};         // its raw list entries of keys lane and lane + 32 (paged: the page)
+    // raw list entries of keys lane and lane + 32 (paged: the page) of the next
+    // tile, and (two sets) of the one after it
+    int next_idx[2] = {-1, -1}, then_idx[2] = {-1, -1};
     if (PAGED) {
       g = ms.start_group;
       t = ms.start_tile;
@@ -370,65 +404,78 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
     auto open_segment = [&]() {
       len = group_len<PAGED>(p, g);
       const int nt = tiles_of(len);
-      te = static_cast<int>(min(static_cast<int64_t>(nt), t + (x1 - x)));
+      te = min(nt, t + left);
       direct = t == 0 && te == nt;
-      slot = blockIdx.x * 2 + (t == 0 ? 1 : 0);
       fresh = true;
       if (t == 0 && te < nt && set == 0 && pt == 0) {
         // the group goes on in the ranges after this one, up to the one that holds its last tile
-        const int64_t last = x + nt - 1;
+        const int64_t last = x1 - left + nt - 1;
         const int c1 = static_cast<int>(((last + 1) * parts - 1) / total);
         p.meta[blockIdx.x] = make_int4(g, c1 - part + 1, 0, 0);
       }
+      from_start = t == 0;
       list = PAGED ? p.block_table + static_cast<int64_t>(g) * p.max_blocks
                    : p.slots + static_cast<int64_t>(g) * p.ld_slots;
-      x += te - t;
+      left -= te - t;
     };
-    auto fetch_idx = [&]() {
+    auto fetch_idx = [&](int tt, int (&to)[2]) {
       if (PAGED) {
-        next_idx[0] = t * kAttnKeys < len ? __ldg(list + t) : -1;  // a tile is a page
+        to[0] = tt < te && tt * kAttnKeys < len ? __ldg(list + tt) : -1;  // a tile is a page
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int j = t * kAttnKeys + h * 32 + lane;
-          next_idx[h] = j < len ? __ldg(list + j) : -1;
+          const int j = tt * kAttnKeys + h * 32 + lane;
+          to[h] = tt < te && j < len ? __ldg(list + j) : -1;
         }
+      }
+    };
+    auto first_idx = [&]() {
+      fetch_idx(t, next_idx);
+      if (FP8) fetch_idx(t + 1, then_idx);
+    };
+    auto shift_idx = [&]() {
+      if (FP8) {
+        next_idx[0] = then_idx[0];
+        next_idx[1] = then_idx[1];
+        fetch_idx(t + 1, then_idx);
+      } else {
+        fetch_idx(t, next_idx);
       }
     };
 
     // ---- the tile about to be written (fp8: its rows on the way in registers)
     Info d;
-    uint4 raw[FP8 ? 20 : 1];
+    uint4 raw[FP8 ? 16 : 1];
     float sc = 0.f;
-    const uint8_t* src[4];
-    const uint8_t* pe_src[4];
-    bool have[4];
+    int row[4];              // pool slots of its rows r0 + 16 k, -1 where there is none
+    const uint8_t* src[4];   // bf16: their addresses
+    const int num_slots = static_cast<int>(p.num_slots), num_pages = num_slots / kPageSize;
     // Finds the next tile that holds keys (or ends a segment, or the stream) and describes it in d.
     auto advance = [&]() {
       for (;;) {
         if (t == te) {
-          if (x == x1) {
+          if (left == 0) {
             d.flags = kEnd;
             return;
           }
           ++g;
           t = 0;
           open_segment();
-          fetch_idx();
+          first_idx();
         }
-        int64_t sl[2];
+        int sl[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          int64_t v = -1;
+          int v = -1;
           if (PAGED) {
             const int pg = next_idx[0];
             if (t * kAttnKeys + h * 32 + lane < len) {
-              if (pg >= 0 && pg < p.num_slots / kPageSize) v = static_cast<int64_t>(pg) * kPageSize + h * 32 + lane;
+              if (pg >= 0 && pg < num_pages) v = pg * kPageSize + h * 32 + lane;
               else bad |= kStatusBadPage;
             }
           } else {
             v = next_idx[h];
-            if (v >= p.num_slots) {
+            if (v >= num_slots) {
               v = -1;
               bad |= kStatusBadSlot;
             }
@@ -441,37 +488,34 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
         d.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (null ? kNull : 0) | (direct ? kDirect : 0);
         d.group = g;
         d.ends = PAGED ? len - p.R + 1 - t * kAttnKeys : 1 << 20;
-        d.piece = slot;
+        d.piece = static_cast<int>(blockIdx.x) * 2 + (from_start ? 1 : 0);
         ++t;
-        if (t < te) fetch_idx();
+        shift_idx();
         if (null && !last) continue;  // nothing to do and nothing to say
         if (!null) {
           fresh = false;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int64_t v = __shfl_sync(0xFFFFFFFFu, sl[k >> 1], (r0 + 16 * k) & 31);
-            have[k] = v >= 0;
-            src[k] = p.kv + (v >= 0 ? v : 0) * kRowBytes + piece * 16;
-            if (FP8) pe_src[k] = p.pe + (v >= 0 ? v : 0) * (kRope * 2) + piece * 16;
+            row[k] = __shfl_sync(0xFFFFFFFFu, sl[k >> 1], (r0 + 16 * k) & 31);
+            if (!FP8) src[k] = p.kv + static_cast<int64_t>(max(row[k], 0)) * kRowBytes + piece * 16;
           }
           if (FP8 && pt < kAttnKeys) {
-            const int64_t v = pt < 32 ? sl[0] : sl[1];
-            // a scale of 0 (or below 2^-60) counts as 2^-60: its log and inverse are used
-            const float x = v >= 0 ? __ldg(p.s + v) : 1.f;
-            sc = x < 8.673617379884035e-19f ? 8.673617379884035e-19f : x;
+            const int v = pt < 32 ? sl[0] : sl[1];
+            sc = v >= 0 ? __ldg(p.s + v) : 1.f;
           }
         }
         return;
       }
     };
-    // fp8: the tile's codes (16 bytes of part c in raw[4 c + k]) and rotated rows.
+    // fp8: the tile's codes (16 bytes of part c in raw[4 c + k]).
     auto load_raw = [&]() {
       if (FP8) {
 #pragma unroll
-        for (int c = 0; c < kParts; ++c)
+        for (int k = 0; k < 4; ++k) {
+          const uint8_t* at = p.kv + static_cast<int64_t>(max(row[k], 0)) * kLatent + piece * 16;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            raw[4 * c + k] = have[k] ? ld_stream16(c < 4 ? src[k] + c * 128 : pe_src[k]) : make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 4; ++c) raw[4 * c + k] = row[k] >= 0 ? ld_stream16(at + c * 128) : make_uint4(0, 0, 0, 0);
+        }
       }
     };
     auto store_part = [&](int c, uint32_t dst) {
@@ -479,30 +523,28 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
       for (int k = 0; k < 4; ++k) {
         const uint32_t rd = dst + k * 2048 + 2 * c * kChunkBytes;
         const uint4 v = raw[FP8 ? 4 * c + k : 0];
-        if (c < 4) {
-          uint32_t a[4], b[4];
-          e4m3x4_f16(v.x, a[0], a[1]);
-          e4m3x4_f16(v.y, a[2], a[3]);
-          e4m3x4_f16(v.z, b[0], b[1]);
-          e4m3x4_f16(v.w, b[2], b[3]);
-          st_shared16(rd + fdst0, odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? b[2] : a[2], odd ? b[3] : a[3]);
-          st_shared16(rd + fdst1, odd ? a[0] : b[0], odd ? a[1] : b[1], odd ? a[2] : b[2], odd ? a[3] : b[3]);
-        } else {
-          st_shared16(rd + swz, v.x, v.y, v.z, v.w);
-        }
+        uint32_t a[4], b[4];
+        e4m3x4_f16(v.x, a[0], a[1]);
+        e4m3x4_f16(v.y, a[2], a[3]);
+        e4m3x4_f16(v.z, b[0], b[1]);
+        e4m3x4_f16(v.w, b[2], b[3]);
+        st_shared16(rd + fdst0, odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? b[2] : a[2], odd ? b[3] : a[3]);
+        st_shared16(rd + fdst1, odd ? a[0] : b[0], odd ? a[1] : b[1], odd ? a[2] : b[2], odd ? a[3] : b[3]);
       }
     };
 
     bool ok = true;
-    if (x < x1) {
+    if (left > 0) {
       open_segment();
-      fetch_idx();
+      first_idx();
     } else {
       t = te;
     }
     advance();
-    if (set == 1 && !(d.flags & kEnd)) advance();
-    else if (set == 1) ok = false;  // set 0 announces the end
+    if (FP8 && set == 1) {
+      if (d.flags & kEnd) ok = false;  // set 0 announces the end
+      else advance();
+    }
     if (FP8 && ok && !(d.flags & (kNull | kEnd))) load_raw();
     for (int i = set; ok; i += FP8 ? 2 : 1) {
       const int st = i & 1;
@@ -583,9 +625,11 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
         if (!FP8) mbar_arrive(&ms.full[st][0]);
       }
       if (FP8 && pt < kAttnKeys) {
-        ms.scale[st][0][pt] = sc;
-        ms.scale[st][1][pt] = log2f(sc);
-        ms.scale[st][2][pt] = 1.f / sc;
+        // a scale of 0 (or below 2^-60) counts as 2^-60: its log and inverse are used
+        const float x = sc < 8.673617379884035e-19f ? 8.673617379884035e-19f : sc;
+        ms.scale[st][0][pt] = x;
+        ms.scale[st][1][pt] = log2f(x);
+        ms.scale[st][2][pt] = 1.f / x;
       }
       if (FP8 && (flags & kFirst) && !null && piece == 0) {
 #pragma unroll
@@ -593,27 +637,48 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
       }
       const bool withhold = p.debug_withhold_first_tile && i == 0;
       const uint32_t dst = row_dst + st * kStageBytes;
+      if (FP8 && !null) {
+        // the rotated part, bf16 as it is: asynchronous copies, on their way while the codes are converted
+        if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, p.status, limit)) break;
 #pragma unroll
-      for (int c = 0; c < kParts; ++c) {
-        if (c > 0 && (flags & kEnd)) break;
-        if (c > 0 && !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
-        if (FP8) {
-          if (!null) store_part(c, dst);
+        for (int k = 0; k < 4; ++k)
+          cp_async16(dst + 8 * kChunkBytes + k * 2048 + swz,
+                     p.pe + static_cast<int64_t>(max(row[k], 0)) * (kRope * 2) + piece * 16, row[k] >= 0 ? 16 : 0);
+        cp_async_arrive(&ms.full[st][4]);
+      }
+#pragma unroll
+      for (int f = 0; f < Sh::kFull; ++f) {
+        if (f > 0 && (flags & kEnd)) break;
+#pragma unroll
+        for (int c = Sh::first_part(f); c < Sh::first_part(f + 1); ++c) {
+          if (c > 0 && !(flags & kEnd) &&
+              !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
+          if (null) continue;
+          if (FP8) {
+            if (c < 4) store_part(c, dst);
+          } else {
+#pragma unroll
+            for (int u = 0; u < (c < 4 ? 2 : 1); ++u)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                cp_async16(dst + (2 * c + u) * kChunkBytes + k * 2048 + swz, src[k] + (2 * c + u) * 128,
+                           row[k] >= 0 ? 16 : 0);
+          }
+        }
+        if (!ok) break;
+        if (FP8 && f < 4) {
           fence_async_shared();
           __syncwarp();
-          if (lane == 0 && !(withhold && c == 0)) mbar_arrive(&ms.full[st][c]);
+          if (lane == 0 && !(withhold && f == 0)) mbar_arrive(&ms.full[st][f]);
+        } else if (FP8 && !null) {
+          // (its copies went out before part 0)
         } else if (null) {
-          mbar_arrive(&ms.full[st][c]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < (c < 4 ? 2 : 1); ++u)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              cp_async16(dst + (2 * c + u) * kChunkBytes + k * 2048 + swz, src[k] + (2 * c + u) * 128,
-                         have[k] ? 16 : 0);
-          if (!(withhold && c == 0)) cp_async_arrive(&ms.full[st][c]);
+          mbar_arrive(&ms.full[st][f]);
+        } else if (!(withhold && f == 0)) {
+          cp_async_arrive(&ms.full[st][f]);
         }
       }
+      if (!ok) break;
       if (flags & kEnd) break;
       // ---- the next tile (fp8: of this set; its loads go out now, with no fence behind them until they are used)
       advance();
@@ -642,7 +707,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
       const int flags = ms.info[i & (kInfo - 1)].flags;
       if (flags & (kNull | kEnd)) {
         bool ok = true;
-        for (int c = 1; c < kParts && ok && !(flags & kEnd); ++c)
+        for (int c = 1; c < Sh::kFull && ok && !(flags & kEnd); ++c)
           ok = warp_wait(&ms.full[st][c], ph, abort_flag, p.status, limit);
         if (!ok) break;
         if (elect_one()) {
@@ -660,18 +725,21 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
       }
       bool ok = true;
 #pragma unroll
-      for (int c = 0; c < kParts; ++c) {
-        if (c > 0 && !warp_wait(&ms.full[st][c], ph, abort_flag, p.status, limit)) { ok = false; break; }
-        if (!FP8) fence_async_shared();  // the rows came by asynchronous copies of other threads
+      for (int f = 0; f < Sh::kFull; ++f) {
+        if (f > 0 && !warp_wait(&ms.full[st][f], ph, abort_flag, p.status, limit)) { ok = false; break; }
+        if (!FP8 || f == 4) fence_async_shared();  // these rows came by asynchronous copies of other threads
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t dd = tbase + (FP8 && c == 4 ? kTmemPe : kTmemS) + st * 64;
 #pragma unroll
-          for (int ks = 0; ks < (c < 4 ? 8 : 4); ++ks) {
-            const int off = ((2 * c + (ks >> 2)) * kChunkBytes + (ks & 3) * 32) >> 4;
-            mma_16(dd, q_d + off, k_d + off, c == 4 ? id_pe : id_s, ks > 0 || (c > 0 && !(FP8 && c == 4)));
+          for (int c = Sh::first_part(f); c < Sh::first_part(f + 1); ++c) {
+            const uint32_t dd = tbase + (FP8 && c == 4 ? kTmemPe : kTmemS) + st * 64;
+#pragma unroll
+            for (int ks = 0; ks < (c < 4 ? 8 : 4); ++ks) {
+              const int off = ((2 * c + (ks >> 2)) * kChunkBytes + (ks & 3) * 32) >> 4;
+              mma_16(dd, q_d + off, k_d + off, c == 4 ? id_pe : id_s, ks > 0 || (c > 0 && !(FP8 && c == 4)));
+            }
           }
-          if (c == 4) {
+          if (f == Sh::kFull - 1) {
             mma_commit(&ms.empty[st][4]);
             mma_commit(&ms.s_full[st]);
           }
@@ -714,11 +782,13 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
     }
     if (elect_one()) mma_commit(&ms.drain);
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp < kSoftmax / 32) {
     // ================================================================ softmax and output
-    const uint32_t lane_base = static_cast<uint32_t>(warp) << 21;  // TMEM lane 32 * warp
-    const int rr = warp * 16 + (lane >> 2);  // this thread's columns (heads): rr and rr + 8
-    const int cq = 2 * (lane & 3);           // its keys: 8 j + cq + {0, 1}
+    const int wg = warp >> 2, quad = warp & 3;                     // keys [kKeys wg, + kKeys); TMEM lane quadrant
+    constexpr int kKeys = 64 / kSwg, NJ = kKeys / 8, NR = 4 * NJ;  // keys, 8-key blocks, scores a thread
+    const uint32_t lane_base = static_cast<uint32_t>(quad) << 21;  // TMEM lane 32 * quad
+    const int rr = quad * 16 + (lane >> 2);        // this thread's columns (heads): rr and rr + 8
+    const int cq = kKeys * wg + 2 * (lane & 3);    // its keys: 8 j + cq + {0, 1}
     const int cols = p.R * p.H;
     int trow[2];                             // row within the group of each column
 #pragma unroll
@@ -726,14 +796,15 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
     // fp8: weights are fp16, whose range the maximum is moved away from the
     // lower end of (2^7 next to it, 2^15 before a rescale; 2^-24 is the smallest)
     constexpr float kBias = FP8 ? 7.f : 0.f;
-    uint8_t* prow = smem + kOffP + rr * 128 + 2 * cq;
+    uint8_t* prow = smem + kOffP + rr * 128 + 4 * (lane & 3);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float to_log2[2] = {p.scale_log2, p.scale_log2};
+    bool dead = false;
     for (int i = 0;; ++i) {
       const int b = i & 1;
-      // a wait that gave up is carried to the votes below, so that all four
+      // a wait that gave up is carried to the votes below, so that all
       // warps leave together
-      bool dead = !warp_wait(&ms.s_full[b], (i >> 1) & 1, abort_flag, p.status, limit);
+      if (!warp_wait(&ms.s_full[b], (i >> 1) & 1, abort_flag, p.status, limit)) dead = true;
       tc_fence_after();
       const Info& f = ms.info[i & (kInfo - 1)];
       const int flags = dead ? kNull : f.flags;
@@ -746,20 +817,56 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
           to_log2[1] = ms.q_scale[b][rr + 8];
         }
       }
-      uint32_t w[16];
-      float fac[2] = {1.f, 1.f};
+      uint32_t w[2 * NJ], r[NR];
+      float mx[2] = {-INFINITY, -INFINITY}, la[2];
+      // The weights of this thread's keys, with the reference maxima as they are, and their sums.
+      auto weigh = [&]() {
+        float neg[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          neg[h] = m[h] == -INFINITY ? 0.f : -m[h];
+          la[h] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          float2 inv;
+          if (FP8) inv = *reinterpret_cast<const float2*>(&ms.scale[b][2][8 * j + cq]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float x = __uint_as_float(r[4 * j + 2 * h]), y = __uint_as_float(r[4 * j + 2 * h + 1]);
+            if (FP8) {
+              const float a = ex2(x + neg[h]), c = ex2(y + neg[h]);
+              // (an unseen key's scale may be anything)
+              la[h] = a == 0.f ? la[h] : fmaf(a, inv.x, la[h]);
+              la[h] = c == 0.f ? la[h] : fmaf(c, inv.y, la[h]);
+              w[2 * j + h] = pack_f16(a, c);
+            } else {
+              const float a = ex2(fmaf(x, to_log2[h], neg[h])), c = ex2(fmaf(y, to_log2[h], neg[h]));
+              la[h] += a + c;
+              w[2 * j + h] = pack_bf16(a, c);
+            }
+          }
+        }
+      };
+      auto put_weights = [&]() {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          *reinterpret_cast<uint32_t*>(prow + (((wg * NJ + j) ^ (rr & 7)) << 4)) = w[2 * j];
+          *reinterpret_cast<uint32_t*>(prow + 8 * 128 + (((wg * NJ + j) ^ (rr & 7)) << 4)) = w[2 * j + 1];
+        }
+      };
       bool grow = false;
-      if (!(flags & (kNull | kEnd))) {
-        uint32_t r[32];
-        tmem_ld_16x64(tbase + kTmemS + b * 64 + lane_base, r);
+      const bool live = !(flags & (kNull | kEnd));
+      if (live) {
+        tmem_ld_16(tbase + kTmemS + b * 64 + wg * kKeys + lane_base, r);
         if (FP8) {
-          uint32_t e[32];
-          tmem_ld_16x64(tbase + kTmemPe + b * 64 + lane_base, e);
+          uint32_t e[NR];
+          tmem_ld_16(tbase + kTmemPe + b * 64 + wg * kKeys + lane_base, e);
           tmem_ld_wait();
           // (codes . q) s + rotated part, in log2 units, plus log2 s: the
           // weight of key j is exp2 of this, i.e. it carries the key's scale
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < NJ; ++j) {
             const float2 v = *reinterpret_cast<const float2*>(&ms.scale[b][0][8 * j + cq]);
             const float2 g = *reinterpret_cast<const float2*>(&ms.scale[b][1][8 * j + cq]);
 #pragma unroll
@@ -778,11 +885,10 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
         mbar_arrive(&ms.s_empty[b]);
         const unsigned long long mask = f.mask;
         const int ends = f.ends;
-        float mx[2] = {-INFINITY, -INFINITY};
         const bool whole = mask == ~0ull && ends >= kAttnKeys;
         if (!whole) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
+          for (int j = 0; j < NR; ++j) {
             const int key = 8 * (j >> 2) + cq + (j & 1), h = (j >> 1) & 1;
             const bool real = (mask >> key) & 1;
             const bool seen = real && key < ends + trow[h];
@@ -799,81 +905,79 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < NJ; ++j) {
           mx[0] = fmaxf(mx[0], fmaxf(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])));
           mx[1] = fmaxf(mx[1], fmaxf(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
         }
-        float neg[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
           mx[h] = (FP8 ? mx[h] : mx[h] * to_log2[h]) - kBias;
-          if (flags & kFirst) {
-            m[h] = mx[h];
-          } else if (mx[h] > m[h] + kRescaleLog2) {
-            fac[h] = ex2(m[h] - mx[h]);
-            m[h] = mx[h];
-            l[h] *= fac[h];
-            grow = true;
-          }
-          neg[h] = m[h] == -INFINITY ? 0.f : -m[h];
+          grow = grow || mx[h] > m[h] + kRescaleLog2;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float2 inv;
-          if (FP8) inv = *reinterpret_cast<const float2*>(&ms.scale[b][2][8 * j + cq]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float x = __uint_as_float(r[4 * j + 2 * h]), y = __uint_as_float(r[4 * j + 2 * h + 1]);
-            if (FP8) {
-              const float a = ex2(x + neg[h]), c = ex2(y + neg[h]);
-              // (an unseen key's scale may be anything)
-              l[h] = a == 0.f ? l[h] : fmaf(a, inv.x, l[h]);
-              l[h] = c == 0.f ? l[h] : fmaf(c, inv.y, l[h]);
-              w[2 * j + h] = pack_f16(a, c);
-            } else {
-              const float a = ex2(fmaf(x, to_log2[h], neg[h])), c = ex2(fmaf(y, to_log2[h], neg[h]));
-              l[h] += a + c;
-              w[2 * j + h] = pack_bf16(a, c);
-            }
-          }
-        }
+        if (!(flags & kFirst)) weigh();
       } else if (!end && !dead) {
         mbar_arrive(&ms.s_empty[b]);
       }
       // the previous value product is done: the weights' buffer is free and the sums hold still
-      if (i > 0 && !dead && !warp_wait(&ms.pv_done, (i - 1) & 1, abort_flag, p.status, limit)) dead = true;
-      if (bar_red_or(1, kSoftmax, dead || end || grow)) {
-        if (bar_red_or(1, kSoftmax, dead || end)) {
-          mbar_arrive(&ms.p_full);  // the value warp sees the end too
-          break;
-        }
-        if ((lane & 3) == 0) {
-          ms.stat_m[rr] = fac[0];
-          ms.stat_m[rr + 8] = fac[1];
-        }
-        named_bar_sync(2, kSoftmax);
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tbase + kTmemO + c * 32 + lane_base, o);
-          tmem_ld_wait();
+      if (i > 0 && !warp_wait(&ms.pv_done, (i - 1) & 1, abort_flag, p.status, limit)) dead = true;
+      if (live && !(flags & kFirst)) put_weights();
+      // One vote: whether some score outgrew its column's reference maximum,
+      // the end, a wait that gave up.  Mostly none did, and the weights taken
+      // with the old maximum stand.
+      const bool vote = bar_red_or(1, kSoftmax, dead || end || grow);
+      if (vote && bar_red_or(1, kSoftmax, dead || end)) {
+        mbar_arrive(&ms.p_full);  // the value warp sees the end too
+        break;
+      }
+      if (live && (vote || (flags & kFirst))) {
+        // ---- new maxima, and the sums so far scaled to them
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            o[k] = __float_as_uint(__uint_as_float(o[k]) * ms.stat_m[(c & 1) * 32 + k]);
-          tmem_st32(tbase + kTmemO + c * 32 + lane_base, o);
+        for (int h = 0; h < 2; ++h) {
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
         }
-        tmem_st_wait();
+        if (kSwg > 1) {
+          if ((lane & 3) == 0) {
+            ms.half_max[b][wg][rr] = mx[0];
+            ms.half_max[b][wg][rr + 8] = mx[1];
+          }
+          named_bar_sync(2, kSoftmax);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (kSwg > 1) mx[h] = fmaxf(mx[h], ms.half_max[b][wg ^ 1][rr + 8 * h]);
+          float fac = 1.f;
+          if (flags & kFirst) {
+            m[h] = mx[h];
+          } else if (mx[h] > m[h] + kRescaleLog2) {
+            fac = ex2(m[h] - mx[h]);
+            m[h] = mx[h];
+            l[h] *= fac;
+          }
+          if ((lane & 3) == 0 && wg == 0) ms.stat_m[rr + 8 * h] = fac;
+        }
+        weigh();
+        put_weights();
+        if (!(flags & kFirst)) {
+          named_bar_sync(2, kSoftmax);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = wg; c < 8; c += kSwg) {
+            uint32_t o[32];
+            tmem_ld32(tbase + kTmemO + c * 32 + lane_base, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              o[k] = __float_as_uint(__uint_as_float(o[k]) * ms.stat_m[(c & 1) * 32 + k]);
+            tmem_st32(tbase + kTmemO + c * 32 + lane_base, o);
+          }
+          tmem_st_wait();
+        }
         named_bar_sync(2, kSoftmax);  // the factors are read before they are written again
       }
-      if (!(flags & kNull)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          *reinterpret_cast<uint32_t*>(prow + ((j ^ (rr & 7)) << 4)) = w[2 * j];
-          *reinterpret_cast<uint32_t*>(prow + 8 * 128 + ((j ^ (rr & 7)) << 4)) = w[2 * j + 1];
-        }
+      if (live) {
+        l[0] += la[0];
+        l[1] += la[1];
         fence_async_shared();
       }
       tc_fence_before();
@@ -887,8 +991,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
         l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
         l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
         if ((lane & 3) == 0) {
-          ms.stat_m[rr + 8 * h] = m[h];
-          ms.stat_l[rr + 8 * h] = l[h];
+          if (wg == 0) ms.stat_m[rr + 8 * h] = m[h];
+          (wg == 0 ? ms.stat_l : ms.stat_l1)[rr + 8 * h] = l[h];
         }
       }
       const bool none = (flags & kNull) && (flags & kFirst);  // no key at all: the sums were never written
@@ -898,65 +1002,69 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) latent_attn_kernel(const _
       tc_fence_after();
       const int n = min(kAttnCols, cols - cg * kAttnCols);
       const int64_t col0 = static_cast<int64_t>(group) * cols + cg * kAttnCols;
-      if (tid < n) {
-        const float mm = ms.stat_m[tid], ll = ms.stat_l[tid];
-        if (!direct) p.part_ml[static_cast<int64_t>(slot) * kAttnCols + tid] = make_float2(mm, ll);
-        else if (p.lse) p.lse[col0 + tid] = (mm + log2f(ll)) * 0.69314718055994531f;
-      }
-      named_bar_sync(2, kSoftmax);
-      if (direct && tid < kAttnCols) {
-        const float ll = ms.stat_l[tid];
-        ms.stat_l[tid] = ll == 0.f ? 0.f : 1.f / ll;
+      if (tid < kAttnCols) {
+        const float mm = ms.stat_m[tid], ll = kSwg > 1 ? ms.stat_l[tid] + ms.stat_l1[tid] : ms.stat_l[tid];
+        if (tid < n) {
+          if (!direct) p.part_ml[static_cast<int64_t>(slot) * kAttnCols + tid] = make_float2(mm, ll);
+          else if (p.lse) p.lse[col0 + tid] = (mm + log2f(ll)) * 0.69314718055994531f;
+        }
+        if (direct) ms.stat_l[tid] = ll == 0.f ? 0.f : 1.f / ll;
       }
       named_bar_sync(2, kSoftmax);
       if (direct) {
-        // 16 values x 64 columns at a time: divided, rounded, transposed
-        // through the warp's quarter of the weights' buffer, and written as
-        // 16-byte pieces (8 values of one column)
-        float inv[16];
+        // 16 values x this warpgroup's columns at a time: divided, rounded,
+        // transposed through the warp's part of the weights' buffer, and
+        // written as 16-byte pieces (8 values of one column)
+        constexpr int NC = kAttnCols / kSwg;
+        const int cb = wg * NC;
+        if (cb < n) {
+          float inv[NC / 4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 v = *reinterpret_cast<const float2*>(&ms.stat_l[8 * j + cq]);
-          inv[2 * j] = v.x;
-          inv[2 * j + 1] = v.y;
-        }
-        uint8_t* tb = smem + kOffP + warp * 2048;
-        const int mrow = (lane >> 4) * 8 + (lane & 7);  // stmatrix: this lane's column (of 16) and value half
-        const uint32_t maddr = smem_u32(tb) + mrow * 32 + ((((lane >> 3) & 1) ^ ((mrow >> 2) & 1)) << 4);
-        uint16_t* oo = p.out + col0 * kLatent + warp * 32;
+          for (int j = 0; j < NC / 8; ++j) {
+            const float2 v = *reinterpret_cast<const float2*>(&ms.stat_l[cb + 8 * j + 2 * (lane & 3)]);
+            inv[2 * j] = v.x;
+            inv[2 * j + 1] = v.y;
+          }
+          uint8_t* tb = smem + kOffP + warp * (NC * 32);
+          const int mrow = (lane >> 4) * 8 + (lane & 7);  // stmatrix: this lane's column (of 16) and value half
+          const uint32_t maddr = smem_u32(tb) + mrow * 32 + ((((lane >> 3) & 1) ^ ((mrow >> 2) & 1)) << 4);
+          uint16_t* oo = p.out + (col0 + cb) * kLatent + quad * 32;
 #pragma unroll 2
-        for (int c = 0; c < 8; ++c) {  // values 128 (c / 2) + 32 warp + 16 (c % 2) + {0 .. 15}
-          uint32_t o[32];
-          if (none) {
+          for (int c = 0; c < 8; ++c) {  // values 128 (c / 2) + 32 quad + 16 (c % 2) + {0 .. 15}
+            uint32_t o[NC / 2];
+            if (none) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0;
-          } else {
-            tmem_ld_16x64(tbase + kTmemO + (c >> 1) * 64 + lane_base + (static_cast<uint32_t>(c & 1) << 20), o);
-            tmem_ld_wait();
-          }
+              for (int k = 0; k < NC / 2; ++k) o[k] = 0;
+            } else {
+              tmem_ld_16(tbase + kTmemO + (c >> 1) * 64 + cb + lane_base + (static_cast<uint32_t>(c & 1) << 20), o);
+              tmem_ld_wait();
+            }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            o[2 * j] = pack_bf16(__uint_as_float(o[4 * j]) * inv[2 * j], __uint_as_float(o[4 * j + 1]) * inv[2 * j + 1]);
-            o[2 * j + 1] =
-                pack_bf16(__uint_as_float(o[4 * j + 2]) * inv[2 * j], __uint_as_float(o[4 * j + 3]) * inv[2 * j + 1]);
-          }
-          __syncwarp();
+            for (int j = 0; j < NC / 8; ++j) {
+              o[2 * j] = pack_bf16(__uint_as_float(o[4 * j]) * inv[2 * j], __uint_as_float(o[4 * j + 1]) * inv[2 * j + 1]);
+              o[2 * j + 1] =
+                  pack_bf16(__uint_as_float(o[4 * j + 2]) * inv[2 * j], __uint_as_float(o[4 * j + 3]) * inv[2 * j + 1]);
+            }
+            __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) stmatrix_x4_trans(maddr + j * 512, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          __syncwarp();
+            for (int j = 0; j < NC / 16; ++j)
+              stmatrix_x4_trans(maddr + j * 512, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int col = k * 16 + (lane >> 1), half = lane & 1;
-            const uint4 v = *reinterpret_cast<const uint4*>(tb + col * 32 + ((half ^ ((col >> 2) & 1)) << 4));
-            if (col < n)
-              *reinterpret_cast<uint4*>(oo + static_cast<int64_t>(col) * kLatent + (c >> 1) * 128 + (c & 1) * 16 + half * 8) = v;
+            for (int k = 0; k < NC / 16; ++k) {
+              const int col = k * 16 + (lane >> 1), half = lane & 1;
+              const uint4 v = *reinterpret_cast<const uint4*>(tb + col * 32 + ((half ^ ((col >> 2) & 1)) << 4));
+              if (cb + col < n)
+                *reinterpret_cast<uint4*>(oo + static_cast<int64_t>(col) * kLatent + (c >> 1) * 128 + (c & 1) * 16 +
+                                          half * 8) = v;
+            }
           }
         }
       } else {
         // [slot][value block, column half][column quad][value][column of the quad]
-        float* po = p.part_o + (static_cast<int64_t>(slot) * 64 * 128 + tid) * 4;
+        float* po = p.part_o + (static_cast<int64_t>(slot) * 64 * 128 + quad * 32 + lane) * 4;
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
+        for (int c = wg; c < 8; c += kSwg) {
           if ((c & 1) * 32 >= n) continue;
           uint32_t o[32];
           if (none) {
@@ -1053,7 +1161,7 @@ cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, 
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   const int grid = p.parts * p.ncg;
-  kern<<<grid, threads_of(fp8), kSmemBytes, st>>>(p);
+  kern<<<grid, fp8 ? Shape<true>::kThreads : Shape<false>::kThreads, kSmemBytes, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

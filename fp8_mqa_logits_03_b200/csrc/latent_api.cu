@@ -164,7 +164,8 @@ int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int6
                                    size_t ws_bytes, void* stream) {
   FP8IDX_TRY(check_latent_shape(H, latent, rope));
   if (rows < 0 || topk < 0) return fail(FP8IDX_EINVAL, "negative size");
-  if (rows > (int64_t(1) << 25) || topk > (1 << 24)) return fail(FP8IDX_EINVAL, "size too large");
+  if (rows > (int64_t(1) << 25) || topk > (1 << 24) || rows * (topk_tiles(topk) + 1) >= (int64_t(1) << 31))
+    return fail(FP8IDX_EINVAL, "size too large");
   FP8IDX_TRY(check_pool(kv_pool, s_pool, pe_pool, num_slots));
   if (rows == 0) return ok();
   if (!q || !out || (topk > 0 && !slots)) return fail(FP8IDX_EINVAL, "null q, slots or out");
