@@ -23,6 +23,8 @@ ks/ke/block_table/seq_lens int32.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -356,47 +358,29 @@ def topk_transform(idx, page_table, page_size: int = 1, row_base=None, row_table
 
 # ---------------------------------------------------------------------------- latent attention
 
-def _rows(t: torch.Tensor, name: str, width: int, dim: int, device=None) -> torch.Tensor:
-    """A bf16 CUDA tensor [..., width] with `dim` dimensions whose last is dense (outer strides are free)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != dim or t.shape[-1] != width:
-        raise ValueError(f"{name} must have {dim} dimensions, the last of {width}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name} must have unit stride in its last dimension")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
+_bind_module = None
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _bind():
+    """The compiled side of the latent calls (tensor checks, outputs, workspace), over the loaded library."""
+    global _bind_module
+    if _bind_module is None:
+        lib()
+        path = os.path.join(_HERE, "_bind.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m fp8_mqa_logits_03_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_bind", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_bind", loader))
+        loader.exec_module(module)
+        module.attach(LIB_PATH)
+        _bind_module = module
+    return _bind_module
 
 
-def _pool(kv_pages, s_pages, pe_pages):
-    """Checks a latent pool; returns its page count."""
-    if (s_pages is None) != (pe_pages is None):
-        raise ValueError("an fp8 pool has both s_pages and pe_pages, a bf16 pool neither")
-    if s_pages is None:
-        _dev(kv_pages, "kv_pages", torch.bfloat16)
-        width = LATENT + ROPE
-    else:
-        _bytes(kv_pages, "kv_pages")
-        _dev(s_pages, "s_pages", torch.float32)
-        _dev(pe_pages, "pe_pages", torch.bfloat16)
-        width = LATENT
-    if kv_pages.dim() != 3 or kv_pages.shape[2] != width:
-        raise ValueError(f"kv_pages must be [pages, {PAGE_SIZE}, {width}], got {tuple(kv_pages.shape)}")
-    pages = kv_pages.shape[0]
-    if s_pages is not None and (s_pages.numel() != pages * kv_pages.shape[1]
-                                or tuple(pe_pages.shape) != (pages, kv_pages.shape[1], ROPE)):
-        raise ValueError("kv_pages, s_pages and pe_pages disagree")
-    _same_device(kv_pages.device, s_pages=s_pages, pe_pages=pe_pages)
-    return pages
+def _result(r):
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def latent_store(c, k_pe, positions, cos_sin, slot_mapping, kv_pages, s_pages=None, pe_pages=None, q_pe=None,
@@ -413,37 +397,9 @@ def latent_store(c, k_pe, positions, cos_sin, slot_mapping, kv_pages, s_pages=No
     (i, 32 + i).  A slot outside the pool is not stored; a token whose
     position is outside the table is left out.  Returns the pool tensors.
     """
-    _pool(kv_pages, s_pages, pe_pages)
-    dev = kv_pages.device
-    if kv_pages.shape[1] != PAGE_SIZE:
-        raise ValueError(f"page size must be {PAGE_SIZE}, got {kv_pages.shape[1]}")
-    c = _rows(c, "c", LATENT, 2, dev)
-    k_pe = _rows(k_pe, "k_pe", ROPE, 2, dev)
-    positions = _dev(positions, "positions", torch.int64)
-    slot_mapping = _dev(slot_mapping, "slot_mapping", torch.int64)
-    cos_sin = _dev(cos_sin, "cos_sin", torch.float32)
-    _same_device(dev, positions=positions, slot_mapping=slot_mapping, cos_sin=cos_sin)
-    T = c.shape[0]
-    if k_pe.shape[0] != T or positions.numel() != T or slot_mapping.numel() != T:
-        raise ValueError("c, k_pe, positions and slot_mapping must have one entry per token")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != ROPE:
-        raise ValueError(f"cos_sin must be [max_pos, {ROPE}]")
-    if (q_pe is None) != (q_out is None):
-        raise ValueError("q_pe and q_out go together")
-    qs = (None, 0, 0, None, 0, 0, 1)
-    if q_pe is not None:
-        q_pe = _rows(q_pe, "q_pe", ROPE, 3, dev)
-        q_out = _rows(q_out, "q_out", ROPE, 3, dev)
-        if q_pe.shape != q_out.shape or q_pe.shape[0] != T:
-            raise ValueError("q_pe and q_out must be [T, H, 64]")
-        qs = (q_pe.data_ptr(), q_pe.stride(0), q_pe.stride(1), q_out.data_ptr(), q_out.stride(0), q_out.stride(1),
-              q_pe.shape[1])
-    with torch.cuda.device(dev):
-        _check(lib().fp8idx_latent_store(c.data_ptr(), c.stride(0), k_pe.data_ptr(), k_pe.stride(0), T,
-                                         positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0],
-                                         1 if interleaved else 0, slot_mapping.data_ptr(),
-                                         kv_pages.shape[0] * PAGE_SIZE, kv_pages.data_ptr(), _ptr(s_pages),
-                                         _ptr(pe_pages), *qs, _stream(stream)))
+    _check((_bind_module or _bind()).latent_store(
+        c, k_pe, positions, cos_sin, slot_mapping, kv_pages, s_pages, pe_pages, q_pe, q_out, interleaved,
+        None if stream is None else stream.cuda_stream))
     return kv_pages if s_pages is None else (kv_pages, s_pages, pe_pages)
 
 
@@ -453,20 +409,6 @@ def sparse_latent_workspace_size(rows: int, heads: int, topk: int) -> int:
 
 def paged_latent_workspace_size(B: int, R: int, max_blocks: int, heads: int) -> int:
     return int(lib().fp8idx_paged_latent_attention_workspace(B, R, max_blocks, heads))
-
-
-def _attn_outputs(q, out, lse, return_lse):
-    rows, heads = q.shape[0], q.shape[1]
-    if out is None:
-        out = torch.empty((rows, heads, LATENT), dtype=torch.bfloat16, device=q.device)
-    elif tuple(_dev(out, "out", torch.bfloat16).shape) != (rows, heads, LATENT):
-        raise ValueError(f"out must be [{rows}, {heads}, {LATENT}]")
-    if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device) if return_lse else None
-    elif tuple(_dev(lse, "lse", torch.float32).shape) != (rows, heads):
-        raise ValueError(f"lse must be [{rows}, {heads}]")
-    _same_device(q.device, out=out, lse=lse)
-    return out, lse
 
 
 def sparse_latent_attention(q, kv_pages, slots, scale: float, s_pages=None, pe_pages=None, out=None, lse=None,
@@ -480,27 +422,9 @@ def sparse_latent_attention(q, kv_pages, slots, scale: float, s_pages=None, pe_p
     the log of each row's sum, [rows, H] float32.  A row without slots gives
     0 and -inf.
     """
-    q = _rows(q, "q", LATENT + ROPE, 3)
-    pages = _pool(kv_pages, s_pages, pe_pages)
-    if not isinstance(slots, torch.Tensor) or not slots.is_cuda or slots.dtype != torch.int32:
-        raise TypeError("slots must be an int32 CUDA tensor")
-    if slots.dim() != 2 or slots.shape[0] != q.shape[0]:
-        raise ValueError("slots must be [rows, topk]")
-    topk = slots.shape[1]
-    if topk > 1 and slots.stride(1) != 1:
-        raise ValueError("slots must have unit column stride")
-    _same_device(q.device, kv_pages=kv_pages, slots=slots, workspace=workspace)
-    out, lse = _attn_outputs(q, out, lse, return_lse)
-    rows, heads = q.shape[0], q.shape[1]
-    ld = max(slots.stride(0), topk) if rows <= 1 else slots.stride(0)
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            workspace = alloc_workspace(sparse_latent_workspace_size(rows, heads, topk), q.device)
-        _check(lib().fp8idx_sparse_latent_attention(
-            q.data_ptr(), q.stride(0), q.stride(1), kv_pages.data_ptr(), _ptr(s_pages), _ptr(pe_pages),
-            pages * kv_pages.shape[1], slots.data_ptr(), ld, rows, topk, heads, LATENT, ROPE, scale, out.data_ptr(),
-            _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream(stream)))
-    return (out, lse) if return_lse else out
+    return _result((_bind_module or _bind()).sparse_latent_attention(
+        q, kv_pages, slots, scale, s_pages, pe_pages, out, lse, workspace, return_lse,
+        None if stream is None else stream.cuda_stream))
 
 
 def paged_latent_attention(q, kv_pages, block_table, seq_lens, R: int, scale: float, s_pages=None, pe_pages=None,
@@ -512,23 +436,6 @@ def paged_latent_attention(q, kv_pages, block_table, seq_lens, R: int, scale: fl
     L = seq_lens[b] sees keys [0, L - R + t + 1).  Pool and results as in
     sparse_latent_attention.
     """
-    q = _rows(q, "q", LATENT + ROPE, 3)
-    pages = _pool(kv_pages, s_pages, pe_pages)
-    block_table = _dev(block_table, "block_table", torch.int32)
-    seq_lens = _dev(seq_lens, "seq_lens", torch.int32)
-    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
-        raise ValueError("block_table must be [B, max_blocks] and seq_lens [B]")
-    B, max_blocks = block_table.shape
-    if q.shape[0] != B * R:
-        raise ValueError(f"q has {q.shape[0]} rows, expected B*R = {B * R}")
-    _same_device(q.device, kv_pages=kv_pages, block_table=block_table, seq_lens=seq_lens, workspace=workspace)
-    out, lse = _attn_outputs(q, out, lse, return_lse)
-    heads = q.shape[1]
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            workspace = alloc_workspace(paged_latent_workspace_size(B, R, max_blocks, heads), q.device)
-        _check(lib().fp8idx_paged_latent_attention(
-            q.data_ptr(), q.stride(0), q.stride(1), kv_pages.data_ptr(), _ptr(s_pages), _ptr(pe_pages),
-            block_table.data_ptr(), seq_lens.data_ptr(), B, R, max_blocks, pages, kv_pages.shape[1], heads, LATENT,
-            ROPE, scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream(stream)))
-    return (out, lse) if return_lse else out
+    return _result((_bind_module or _bind()).paged_latent_attention(
+        q, kv_pages, block_table, seq_lens, R, scale, s_pages, pe_pages, out, lse, workspace, return_lse,
+        None if stream is None else stream.cuda_stream))

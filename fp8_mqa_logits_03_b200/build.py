@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -11,6 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8idx.so")
 SOURCES = ["kernels.cu", "quant.cu", "index_prep.cu", "latent_store.cu", "latent.cu", "latent_api.cu", "api.cu"]
+BIND = os.path.join(HERE, "_bind.so")  # the compiled Python side of the latent calls
 DEPS = SOURCES + ["api_common.h", "kernels.cuh", "latent.cuh", "ptx.cuh", "select.cuh", "wait.cuh"]
 HEADER = os.path.join(os.path.dirname(HERE), "include", "fp8idx.h")
 # the headers each source includes (its object is rebuilt when one changes)
@@ -41,7 +43,24 @@ def _newer(target: str, deps) -> bool:
 
 
 def _stale() -> bool:
-    return _newer(LIB, [os.path.join(CSRC, f) for f in DEPS] + [HEADER])
+    return (_newer(LIB, [os.path.join(CSRC, f) for f in DEPS] + [HEADER])
+            or _newer(BIND, [os.path.join(CSRC, "bind.cpp"), HEADER]))
+
+
+def build_bind() -> None:
+    """Compile csrc/bind.cpp against this interpreter and its torch (host code only)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    tmp = BIND + f".tmp{os.getpid()}"
+    subprocess.check_call(
+        [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-I" + os.path.join(root, "include"), "-I" + os.path.join(cuda, "include"),
+         "-I" + sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "bind.cpp"),
+         "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"],
+        cwd=HERE)
+    os.replace(tmp, BIND)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -63,8 +82,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
             os.replace(tmp, obj)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as pool:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as pool:
+        bind = None
+        if force or _newer(BIND, [os.path.join(CSRC, "bind.cpp"), HEADER]):
+            bind = pool.submit(build_bind)
         objs = list(pool.map(compile_one, SOURCES))
+        if bind is not None:
+            bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-Xcompiler", "-fPIC",
                            "-shared", "-cudart", "static", "-o", tmp, *objs], cwd=HERE)

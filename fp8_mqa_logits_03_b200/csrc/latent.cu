@@ -115,6 +115,8 @@ struct Misc {
   float stat_m[kAttnCols], stat_l[kAttnCols];
   uint32_t tmem;
   int abort_flag;
+  int status;       // device status bits of this CTA
+  int2 cut;         // (group, pieces) of the cut group whose first piece this CTA holds
   int scan[kMaxThreads / 32];
   int start_group, start_tile;
 };
@@ -310,15 +312,19 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     mbar_init(&ms.pv_done, 1);
     mbar_init(&ms.drain, 2);
     ms.abort_flag = 0;
+    ms.status = 0;
+    ms.cut = make_int2(0, 0);
     fence_mbar_init();
-    p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   if (warp == kScoreWarp) {
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
 
+  griddep_wait();  // the inputs are ready, and nobody reads this workspace any more
+
   // ---- this CTA's range of the tile axis
+  bool too_long = false;
   int64_t total;
   if (PAGED) {
     // prefix sum over the requests: each thread a contiguous run of them
@@ -327,8 +333,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     int mine = 0;
     for (int g = g0; g < g1; ++g) {
       mine += tiles_of(group_len<true>(p, g));
-      if (cg == 0 && part == 0 && __ldg(p.seq_lens + g) > static_cast<int64_t>(p.max_blocks) * kPageSize)
-        atomicOr(p.status, kStatusSeqLenTooLong);
+      too_long = too_long || __ldg(p.seq_lens + g) > p.max_blocks * kPageSize;
     }
     int inc = mine;
 #pragma unroll
@@ -368,6 +373,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
   const int64_t x0 = part < parts ? part * total / parts : 0;
   const int64_t x1 = part < parts ? (part + 1) * total / parts : 0;
   const uint32_t tbase = ms.tmem;
+  if (too_long) atomicOr(&ms.status, kStatusSeqLenTooLong);
 
   if (warp >= kSoftmax / 32 && warp < kScoreWarp) {
     // ================================================================ producers
@@ -411,7 +417,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         // the group goes on in the ranges after this one, up to the one that holds its last tile
         const int64_t last = x1 - left + nt - 1;
         const int c1 = static_cast<int>(((last + 1) * parts - 1) / total);
-        p.meta[blockIdx.x] = make_int4(g, c1 - part + 1, 0, 0);
+        ms.cut = make_int2(g, c1 - part + 1);
       }
       from_start = t == 0;
       list = PAGED ? p.block_table + static_cast<int64_t>(g) * p.max_blocks
@@ -557,8 +563,8 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         // of tile i - 1 are done.  Tile i - 2's first: only then is the other
         // barrier's phase the one asked for or the one before it (a set sees
         // every second tile alone).
-        if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, p.status, limit)) break;
-        if (i > 0 && !warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, p.status, limit)) break;
+        if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit)) break;
+        if (i > 0 && !warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) break;
         const int cols = p.R * p.H;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
       // ---- describe the tile.  The entry was tile i - 4's; the values of
       // tile i - 2 have begun, so every role is past tile i - 4.
-      if (!warp_wait(&ms.empty[st][0], ph ^ 1, abort_flag, p.status, limit)) break;
+      if (!warp_wait(&ms.empty[st][0], ph ^ 1, abort_flag, &ms.status, limit)) break;
       if (pt == 0) {
         ms.info[i & (kInfo - 1)] = d;
         if (!FP8) mbar_arrive(&ms.full[st][0]);
@@ -639,7 +645,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const uint32_t dst = row_dst + st * kStageBytes;
       if (FP8 && !null) {
         // the rotated part, bf16 as it is: asynchronous copies, on their way while the codes are converted
-        if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, p.status, limit)) break;
+        if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit)) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           cp_async16(dst + 8 * kChunkBytes + k * 2048 + swz,
@@ -652,7 +658,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 #pragma unroll
         for (int c = Sh::first_part(f); c < Sh::first_part(f + 1); ++c) {
           if (c > 0 && !(flags & kEnd) &&
-              !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, p.status, limit)) { ok = false; break; }
+              !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
           if (null) continue;
           if (FP8) {
             if (c < 4) store_part(c, dst);
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
     }
     cp_async_wait_all();
-    if (bad && cg == 0) atomicOr(p.status, bad);
+    if (bad) atomicOr(&ms.status, bad);
   } else if (warp == kScoreWarp) {
     // ================================================================ score products
     // A whole warp runs the issue loops, so that descriptors and branches are
@@ -702,13 +708,13 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const int st = i & 1;
       const uint32_t ph = (i >> 1) & 1;
       const uint64_t k_d = smem_desc_k128_sw128(smem_u32(smem + kOffK + st * kStageBytes));
-      if (!warp_wait(&ms.s_empty[st], ph ^ 1, abort_flag, p.status, limit)) break;
-      if (!warp_wait(&ms.full[st][0], ph, abort_flag, p.status, limit)) break;
+      if (!warp_wait(&ms.s_empty[st], ph ^ 1, abort_flag, &ms.status, limit)) break;
+      if (!warp_wait(&ms.full[st][0], ph, abort_flag, &ms.status, limit)) break;
       const int flags = ms.info[i & (kInfo - 1)].flags;
       if (flags & (kNull | kEnd)) {
         bool ok = true;
         for (int c = 1; c < Sh::kFull && ok && !(flags & kEnd); ++c)
-          ok = warp_wait(&ms.full[st][c], ph, abort_flag, p.status, limit);
+          ok = warp_wait(&ms.full[st][c], ph, abort_flag, &ms.status, limit);
         if (!ok) break;
         if (elect_one()) {
           if (!(flags & kEnd)) mbar_arrive(&ms.empty[st][4]);
@@ -719,14 +725,14 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         continue;
       }
       if (flags & kFirst) {
-        if (!warp_wait(&ms.q_full, nq & 1, abort_flag, p.status, limit)) break;
+        if (!warp_wait(&ms.q_full, nq & 1, abort_flag, &ms.status, limit)) break;
         ++nq;
         if (!FP8) fence_async_shared();  // the queries came by asynchronous copies of other threads
       }
       bool ok = true;
 #pragma unroll
       for (int f = 0; f < Sh::kFull; ++f) {
-        if (f > 0 && !warp_wait(&ms.full[st][f], ph, abort_flag, p.status, limit)) { ok = false; break; }
+        if (f > 0 && !warp_wait(&ms.full[st][f], ph, abort_flag, &ms.status, limit)) { ok = false; break; }
         if (!FP8 || f == 4) fence_async_shared();  // these rows came by asynchronous copies of other threads
         tc_fence_after();
         if (elect_one()) {
@@ -756,7 +762,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     const uint64_t p_d = smem_desc_k128_sw128(smem_u32(smem + kOffP));
     for (int i = 0;; ++i) {
       const int st = i & 1;
-      if (!warp_wait(&ms.p_full, i & 1, abort_flag, p.status, limit)) break;
+      if (!warp_wait(&ms.p_full, i & 1, abort_flag, &ms.status, limit)) break;
       const int flags = ms.info[i & (kInfo - 1)].flags;
       if (flags & kEnd) break;
       tc_fence_after();
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const int b = i & 1;
       // a wait that gave up is carried to the votes below, so that all
       // warps leave together
-      if (!warp_wait(&ms.s_full[b], (i >> 1) & 1, abort_flag, p.status, limit)) dead = true;
+      if (!warp_wait(&ms.s_full[b], (i >> 1) & 1, abort_flag, &ms.status, limit)) dead = true;
       tc_fence_after();
       const Info& f = ms.info[i & (kInfo - 1)];
       const int flags = dead ? kNull : f.flags;
@@ -919,7 +925,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         mbar_arrive(&ms.s_empty[b]);
       }
       // the previous value product is done: the weights' buffer is free and the sums hold still
-      if (i > 0 && !warp_wait(&ms.pv_done, (i - 1) & 1, abort_flag, p.status, limit)) dead = true;
+      if (i > 0 && !warp_wait(&ms.pv_done, (i - 1) & 1, abort_flag, &ms.status, limit)) dead = true;
       if (live && !(flags & kFirst)) put_weights();
       // One vote: whether some score outgrew its column's reference maximum,
       // the end, a wait that gave up.  Mostly none did, and the weights taken
@@ -997,7 +1003,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
       const bool none = (flags & kNull) && (flags & kFirst);  // no key at all: the sums were never written
       const bool direct = flags & kDirect;
-      if (!warp_wait(&ms.pv_done, i & 1, abort_flag, p.status, limit)) dead = true;
+      if (!warp_wait(&ms.pv_done, i & 1, abort_flag, &ms.status, limit)) dead = true;
       if (bar_red_or(1, kSoftmax, dead)) break;
       tc_fence_after();
       const int n = min(kAttnCols, cols - cg * kAttnCols);
@@ -1092,6 +1098,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0) p.meta[blockIdx.x] = make_int4(ms.cut.x, ms.cut.y, ms.status, 0);
   if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
@@ -1106,6 +1113,16 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 __global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_constant__ LatentAttnParams p) {
   __shared__ float4 wt[kAttnMaxParts];
   griddep_wait();
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    // the call's status block: every CTA's bits
+    int bits = 0;
+    for (int k = threadIdx.x; k < static_cast<int>(gridDim.x); k += 128) bits |= p.meta[k].z;
+    bits = __syncthreads_or(bits & kStatusWaitTimeout) * kStatusWaitTimeout |
+           __syncthreads_or(bits & kStatusBadPage) * kStatusBadPage |
+           __syncthreads_or(bits & kStatusSeqLenTooLong) * kStatusSeqLenTooLong |
+           __syncthreads_or(bits & kStatusBadSlot) * kStatusBadSlot;
+    if (threadIdx.x < kStatusBytes / 4) p.status[threadIdx.x] = threadIdx.x == 0 ? bits : 0;
+  }
   const int4 mt = p.meta[blockIdx.x];
   if (mt.y < 2) return;
   const int cols = p.R * p.H, cg = blockIdx.x % p.ncg;
@@ -1156,24 +1173,34 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_consta
 }
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, cudaStream_t st) {
-  auto kern = paged ? (fp8 ? latent_attn_kernel<true, true> : latent_attn_kernel<true, false>)
-                    : (fp8 ? latent_attn_kernel<false, true> : latent_attn_kernel<false, false>);
+  const void* kern =
+      paged ? (fp8 ? reinterpret_cast<const void*>(latent_attn_kernel<true, true>)
+                   : reinterpret_cast<const void*>(latent_attn_kernel<true, false>))
+            : (fp8 ? reinterpret_cast<const void*>(latent_attn_kernel<false, true>)
+                   : reinterpret_cast<const void*>(latent_attn_kernel<false, false>));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
+  // Both launches are programmatic dependents: a launch's latency overlaps the
+  // end of the kernel before it, whose results it waits for on the device.
   const int grid = p.parts * p.ncg;
-  kern<<<grid, fp8 ? Shape<true>::kThreads : Shape<false>::kThreads, kSmemBytes, st>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 64);  // four value blocks x 16 column quads
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(fp8 ? Shape<true>::kThreads : Shape<false>::kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, latent_combine_kernel, p);
+  LatentAttnParams copy = p;
+  void* args[] = {&copy};
+  e = cudaLaunchKernelExC(&cfg, kern, args);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 64);  // four value blocks x 16 column quads
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(latent_combine_kernel), args);
 }
 
 }  // namespace fp8idx

@@ -63,7 +63,7 @@ struct LatentAttnParams {
   int* status;
   float* part_o;            // [grid][2][64 x 512] unnormalised sums of cut groups
   float2* part_ml;          // [grid][2][64] (reference maximum in log2 units, sum)
-  int4* meta;               // [grid] (group, pieces, -, -) of the cut group whose first piece the CTA holds
+  int4* meta;               // [grid] (group, pieces) of the cut group whose first piece the CTA holds, status bits
   unsigned long long wait_limit_ns;
   int debug_withhold_first_tile;
 };

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -16,6 +17,17 @@
 namespace {
 
 using namespace fp8idx;
+
+// The SM count of the current device, asked for once per device.
+int sms_cached() {
+  static std::atomic<int> of[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 0 || dev >= 64) return device_sms();
+  int n = of[dev].load(std::memory_order_relaxed);
+  if (n <= 0) of[dev].store(n = device_sms(), std::memory_order_relaxed);
+  return n;
+}
 
 struct AttnPlan {
   int ncg = 1, parts = 1;
@@ -85,9 +97,7 @@ int run_attn(LatentAttnParams& p, const AttnPlan& pl, bool paged, bool fp8, void
   p.wait_limit_ns = g_wait_limit_ns;
   p.debug_withhold_first_tile = g_debug_withhold;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(ws, 0, kStatusBytes, st);
-  if (e != cudaSuccess) return cuda_fail(e, "status reset");
-  e = launch_latent_attn(p, fp8, paged, st);
+  cudaError_t e = launch_latent_attn(p, fp8, paged, st);
   if (e != cudaSuccess) return cuda_fail(e, "latent attention launch");
   return ok();
 }
@@ -152,7 +162,7 @@ int fp8idx_latent_store(const uint16_t* c, int64_t c_stride, const uint16_t* k_p
 
 size_t fp8idx_sparse_latent_attention_workspace(int64_t rows, int H, int topk) {
   if (rows < 0 || H < 1 || H > kAttnMaxHeads || topk < 0) return 0;
-  const int sms = device_sms();
+  const int sms = sms_cached();
   if (sms <= 0) return 0;
   return plan_attn(rows, H, topk_tiles(topk), sms).total;
 }
@@ -173,7 +183,7 @@ int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int6
   FP8IDX_TRY(check_strides("q", q, q_row_stride, q_head_stride));
   if (!aligned(out, 16) || !aligned(slots, 4) || !aligned(lse, 4))
     return fail(FP8IDX_EINVAL, "out must be 16-byte aligned, slots and lse 4-byte aligned");
-  const int sms = device_sms();
+  const int sms = sms_cached();
   if (sms <= 0) return fail(FP8IDX_ECUDA, "no CUDA device");
   LatentAttnParams p;
   memset(&p, 0, sizeof(p));
@@ -197,7 +207,7 @@ int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int6
 
 size_t fp8idx_paged_latent_attention_workspace(int64_t B, int R, int max_blocks, int H) {
   if (B < 0 || R < 1 || R > 8 || H < 1 || H > kAttnMaxHeads || max_blocks < 1) return 0;
-  const int sms = device_sms();
+  const int sms = sms_cached();
   if (sms <= 0) return 0;
   return plan_attn(B, static_cast<int64_t>(R) * H, max_blocks, sms).total;
 }
@@ -221,7 +231,7 @@ int fp8idx_paged_latent_attention(const uint16_t* q, int64_t q_row_stride, int64
   FP8IDX_TRY(check_strides("q", q, q_row_stride, q_head_stride));
   if (!aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4))
     return fail(FP8IDX_EINVAL, "out must be 16-byte aligned, block_table, seq_lens and lse 4-byte aligned");
-  const int sms = device_sms();
+  const int sms = sms_cached();
   if (sms <= 0) return fail(FP8IDX_ECUDA, "no CUDA device");
   LatentAttnParams p;
   memset(&p, 0, sizeof(p));
