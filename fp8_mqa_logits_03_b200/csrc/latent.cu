@@ -59,9 +59,9 @@ struct Shape {
   static constexpr int kSoftmax = 128 * kSwg;
   static constexpr int kSets = FP8 ? 2 : 1;       // producer sets
   static constexpr int kThreads = kSoftmax + kSets * kSet + 64;
-  static constexpr int kFull = FP8 ? 5 : 2;       // announcements of a tile's parts
+  static constexpr int kFull = FP8 ? 3 : 2;       // announcements of a tile's parts
   // the parts that announcement f covers
-  __host__ __device__ static constexpr int first_part(int f) { return FP8 ? f : (f == 0 ? 0 : f == 1 ? 2 : 5); }
+  __host__ __device__ static constexpr int first_part(int f) { return f == 0 ? 0 : f == 1 ? 2 : FP8 && f == 2 ? 4 : 5; }
 };
 constexpr int kMaxThreads = 448;
 static_assert(Shape<true>::kThreads <= kMaxThreads && Shape<false>::kThreads <= kMaxThreads, "threads");
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     for (int s = 0; s < kStages; ++s)
       for (int i = 0; i < kParts; ++i) {
         // codes: one arrival a warp; asynchronous copies: one a thread (bf16: and one with the tile's description)
-        mbar_init(&ms.full[s][i], FP8 && i < 4 ? kSet / 32 : kSet + (i == 0 ? 1 : 0));
+        mbar_init(&ms.full[s][i], FP8 && i < 2 ? kSet / 32 : kSet + (i == 0 ? 1 : 0));
         mbar_init(&ms.empty[s][i], 1);
       }
     mbar_init(&ms.q_full, kSet);
@@ -539,10 +539,73 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
     };
 
+    // ---- the group's query columns
+    auto copy_q = [&](int group) {
+      const int cols = p.R * p.H;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int col = cg * kAttnCols + r0 + 16 * k;
+        const bool v = col < cols;
+        const int qr = PAGED && v ? col / p.H : 0, h = v ? col - qr * p.H : 0;
+        const uint8_t* qs = reinterpret_cast<const uint8_t*>(
+            p.q + (static_cast<int64_t>(group) * p.R + qr) * p.q_row + h * p.q_head) + piece * 16;
+        const uint32_t qd = smem_u32(smem + kOffQ) + (r0 + 16 * k) * 128 + swz;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) cp_async16(qd + c * kChunkBytes, qs + c * 128, v ? 16 : 0);
+      }
+    };
+    // fp8: the codes are products' other side in fp16, so a column becomes
+    // fp16 too, in place, times the power of two that brings its largest value
+    // next to 2^14: exact but for values 2^28 times smaller, whose error
+    // (2^-39 of the largest) is below the fp32 sum's.  The rotated part meets
+    // bf16 and stays bf16.  A thread converts the pieces that it copied.
+    auto convert_q = [&](float (&fac)[4]) {
+      cp_async_wait_all();
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        uint8_t* at = smem + kOffQ + (r0 + 16 * k) * 128 + swz;
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(at + c * kChunkBytes);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t y = (&v.x)[e] & 0x7FFF7FFFu;
+            top = max(top, max(y & 0xFFFFu, y >> 16));
+          }
+        }
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+        const int ex = top >> 7;  // biased exponent of the largest value
+        // times 2^(140 - ex), as two factors that are ordinary numbers; a zero or non-finite column stays
+        const int up = ex == 0 || ex == 255 ? 0 : 140 - ex, up0 = up / 2, up1 = up - up0;
+        const float f0 = __uint_as_float(static_cast<uint32_t>(127 + up0) << 23);
+        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up1) << 23);
+        fac[k] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up0) << 23) *
+                 __uint_as_float(static_cast<uint32_t>(127 - up1) << 23);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          uint4 v = *reinterpret_cast<const uint4*>(at + c * kChunkBytes);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t y = (&v.x)[e];
+            const float lo = __uint_as_float(y << 16) * f0 * f1, hi = __uint_as_float(y & 0xFFFF0000u) * f0 * f1;
+            (&v.x)[e] = c < 8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+          }
+          *reinterpret_cast<uint4*>(at + c * kChunkBytes) = v;
+        }
+      }
+      fence_async_shared();
+      mbar_arrive(&ms.q_full);
+    };
+
     bool ok = true;
     if (left > 0) {
       open_segment();
       first_idx();
+      // on its way while the first list entries are; used if tile 0 holds keys (it is then of this group)
+      if (set == 0) copy_q(g);
     } else {
       t = te;
     }
@@ -557,71 +620,20 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const uint32_t ph = (i >> 1) & 1;
       const int flags = d.flags;
       const bool null = flags & (kNull | kEnd);
-      float qfac[4];
-      if ((flags & kFirst) && !null) {
+      if ((flags & kFirst) && !null && i > 0) {
         // ---- the group's query columns; their place is free once the scores
         // of tile i - 1 are done.  Tile i - 2's first: only then is the other
         // barrier's phase the one asked for or the one before it (a set sees
         // every second tile alone).
         if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit)) break;
-        if (i > 0 && !warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) break;
-        const int cols = p.R * p.H;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int col = cg * kAttnCols + r0 + 16 * k;
-          const bool v = col < cols;
-          const int row = v ? col / p.H : 0, h = v ? col - row * p.H : 0;
-          const uint8_t* qs = reinterpret_cast<const uint8_t*>(
-              p.q + (static_cast<int64_t>(d.group) * p.R + row) * p.q_row + h * p.q_head) + piece * 16;
-          const uint32_t qd = smem_u32(smem + kOffQ) + (r0 + 16 * k) * 128 + swz;
-          if (!FP8) {
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) cp_async16(qd + c * kChunkBytes, qs + c * 128, v ? 16 : 0);
-          } else {
-            // The codes are products' other side in fp16, so a column becomes
-            // fp16 too, times the power of two that brings its largest value
-            // next to 2^14: exact but for values 2^28 times smaller, whose
-            // error (2^-39 of the largest) is below the fp32 sum's.
-            uint32_t m = 0;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-              const uint4 x = v ? __ldg(reinterpret_cast<const uint4*>(qs + c * 128)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t y = (&x.x)[e] & 0x7FFF7FFFu;
-                m = max(m, max(y & 0xFFFFu, y >> 16));
-              }
-            }
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-            const int ex = m >> 7;  // biased exponent of the largest value
-            // times 2^(140 - ex), as two factors that are ordinary numbers; a zero or non-finite column stays
-            const int up = ex == 0 || ex == 255 ? 0 : 140 - ex, up0 = up / 2, up1 = up - up0;
-            const float f0 = __uint_as_float(static_cast<uint32_t>(127 + up0) << 23);
-            const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up1) << 23);
-            qfac[k] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up0) << 23) *
-                      __uint_as_float(static_cast<uint32_t>(127 - up1) << 23);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-              const uint4 x = v ? __ldg(reinterpret_cast<const uint4*>(qs + c * 128)) : make_uint4(0, 0, 0, 0);
-              uint32_t o[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t y = (&x.x)[e];
-                const float lo = __uint_as_float(y << 16) * f0 * f1, hi = __uint_as_float(y & 0xFFFF0000u) * f0 * f1;
-                o[e] = c < 8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);  // the rotated part meets bf16
-              }
-              st_shared16(qd + c * kChunkBytes, o[0], o[1], o[2], o[3]);
-            }
-          }
-        }
-        if (FP8) {
-          fence_async_shared();
-          mbar_arrive(&ms.q_full);
-        } else {
-          cp_async_arrive(&ms.q_full);
-        }
+        if (!warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) break;
+        copy_q(d.group);
+      }
+      if (i == 0 && null) cp_async_wait_all();  // the queries copied ahead are not used: out of the way of the next ones
+      float qfac[4];
+      if ((flags & kFirst) && !null) {
+        if (FP8) convert_q(qfac);
+        else cp_async_arrive(&ms.q_full);
       }
       // ---- describe the tile.  The entry was tile i - 4's; the values of
       // tile i - 2 have begun, so every role is past tile i - 4.
@@ -650,7 +662,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         for (int k = 0; k < 4; ++k)
           cp_async16(dst + 8 * kChunkBytes + k * 2048 + swz,
                      p.pe + static_cast<int64_t>(max(row[k], 0)) * (kRope * 2) + piece * 16, row[k] >= 0 ? 16 : 0);
-        cp_async_arrive(&ms.full[st][4]);
+        cp_async_arrive(&ms.full[st][2]);
       }
 #pragma unroll
       for (int f = 0; f < Sh::kFull; ++f) {
@@ -672,7 +684,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           }
         }
         if (!ok) break;
-        if (FP8 && f < 4) {
+        if (FP8 && f < 2) {
           fence_async_shared();
           __syncwarp();
           if (lane == 0 && !(withhold && f == 0)) mbar_arrive(&ms.full[st][f]);
@@ -733,7 +745,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 #pragma unroll
       for (int f = 0; f < Sh::kFull; ++f) {
         if (f > 0 && !warp_wait(&ms.full[st][f], ph, abort_flag, &ms.status, limit)) { ok = false; break; }
-        if (!FP8 || f == 4) fence_async_shared();  // these rows came by asynchronous copies of other threads
+        if (!FP8 || f == 2) fence_async_shared();  // these rows came by asynchronous copies of other threads
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -1035,16 +1047,22 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           const int mrow = (lane >> 4) * 8 + (lane & 7);  // stmatrix: this lane's column (of 16) and value half
           const uint32_t maddr = smem_u32(tb) + mrow * 32 + ((((lane >> 3) & 1) ^ ((mrow >> 2) & 1)) << 4);
           uint16_t* oo = p.out + (col0 + cb) * kLatent + quad * 32;
-#pragma unroll 2
-          for (int c = 0; c < 8; ++c) {  // values 128 (c / 2) + 32 quad + 16 (c % 2) + {0 .. 15}
-            uint32_t o[NC / 2];
-            if (none) {
+          uint32_t o[NC / 2], ahead[NC / 2];
+          auto fetch = [&](int c) {
+            tmem_ld_16(tbase + kTmemO + (c >> 1) * 64 + cb + lane_base + (static_cast<uint32_t>(c & 1) << 20), ahead);
+          };
+          if (none) {
 #pragma unroll
-              for (int k = 0; k < NC / 2; ++k) o[k] = 0;
-            } else {
-              tmem_ld_16(tbase + kTmemO + (c >> 1) * 64 + cb + lane_base + (static_cast<uint32_t>(c & 1) << 20), o);
-              tmem_ld_wait();
-            }
+            for (int k = 0; k < NC / 2; ++k) ahead[k] = 0;
+          } else {
+            fetch(0);
+          }
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {  // values 128 (c / 2) + 32 quad + 16 (c % 2) + {0 .. 15}
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < NC / 2; ++k) o[k] = ahead[k];
+            if (!none && c < 7) fetch(c + 1);
 #pragma unroll
             for (int j = 0; j < NC / 8; ++j) {
               o[2 * j] = pack_bf16(__uint_as_float(o[4 * j]) * inv[2 * j], __uint_as_float(o[4 * j + 1]) * inv[2 * j + 1]);
@@ -1107,69 +1125,133 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 
 // ---------------------------------------------------------------- joining cut groups
 
-// Block (x, y): the group whose first piece CTA x holds, value block y / 16,
-// columns [4 (y % 16), + 4).  The pieces lie in the CTAs x, x + ncg, ..., in
-// key order: the first in its second slot, the others in their first.
-__global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_constant__ LatentAttnParams p) {
-  __shared__ float4 wt[kAttnMaxParts];
+// Block (x, y): the group whose first piece CTA x holds, value block y % 4,
+// columns [4 QPB (y / 4), + 4 QPB).  The pieces lie in the CTAs x, x + ncg,
+// ..., in key order: the first in its second slot, the others in their first.
+// Four sets of 128 threads, one value each.  With few pieces a set takes a
+// column quad of its own; with many (a long group over all SMs) it takes every
+// fourth piece, and the sets' sums are joined.  A thread's first loads go out
+// before the weights are known.  QPB is 4, or 1 where few groups can be cut:
+// more blocks then share a group's pieces.
+constexpr int kJoinThreads = 512, kJoinAhead = 8;
+constexpr int kSpreadGroups = 8;  // "few groups"
+
+template <int QPB>
+__global__ void __launch_bounds__(kJoinThreads) latent_combine_kernel(const __grid_constant__ LatentAttnParams p) {
+  __shared__ float4 wt[kAttnMaxParts][QPB];
+  __shared__ float4 acc_of[3][128];
   griddep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     // the call's status block: every CTA's bits
     int bits = 0;
-    for (int k = threadIdx.x; k < static_cast<int>(gridDim.x); k += 128) bits |= p.meta[k].z;
-    bits = __syncthreads_or(bits & kStatusWaitTimeout) * kStatusWaitTimeout |
-           __syncthreads_or(bits & kStatusBadPage) * kStatusBadPage |
-           __syncthreads_or(bits & kStatusSeqLenTooLong) * kStatusSeqLenTooLong |
-           __syncthreads_or(bits & kStatusBadSlot) * kStatusBadSlot;
-    if (threadIdx.x < kStatusBytes / 4) p.status[threadIdx.x] = threadIdx.x == 0 ? bits : 0;
+    for (int k = tid; k < static_cast<int>(gridDim.x); k += kJoinThreads) bits |= p.meta[k].z;
+    bits = (__syncthreads_or(bits & kStatusWaitTimeout) ? kStatusWaitTimeout : 0) |
+           (__syncthreads_or(bits & kStatusBadPage) ? kStatusBadPage : 0) |
+           (__syncthreads_or(bits & kStatusSeqLenTooLong) ? kStatusSeqLenTooLong : 0) |
+           (__syncthreads_or(bits & kStatusBadSlot) ? kStatusBadSlot : 0);
+    if (tid < kStatusBytes / 4) p.status[tid] = tid == 0 ? bits : 0;
   }
   const int4 mt = p.meta[blockIdx.x];
-  if (mt.y < 2) return;
+  const int np = mt.y;
+  if (np < 2) return;
   const int cols = p.R * p.H, cg = blockIdx.x % p.ncg;
   const int n = min(kAttnCols, cols - cg * kAttnCols);
-  const int quad = blockIdx.y & 15, vb = blockIdx.y >> 4;
-  if (4 * quad >= n) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t oc = static_cast<int64_t>(mt.x) * cols + cg * kAttnCols + 4 * quad;
+  const int q0 = (blockIdx.y >> 2) * QPB, vb = blockIdx.y & 3;
+  const int nq = min(QPB, (n + 3) / 4 - q0);  // column quads of this block
+  if (nq <= 0) return;
+  const int64_t oc = static_cast<int64_t>(mt.x) * cols + cg * kAttnCols;
   auto slot_at = [&](int k) { return static_cast<int64_t>(blockIdx.x + k * p.ncg) * 2 + (k == 0 ? 1 : 0); };
-  {
-    // warp w: the weights of column 4 quad + w in every piece
-    const int col = 4 * quad + warp;
+  const int sub = tid >> 7, val = tid & 127;
+  auto at = [&](int quad, int k) {
+    return *reinterpret_cast<const float4*>(p.part_o + slot_at(k) * (kAttnCols * kLatent) +
+                                            ((vb * 2 + (quad >> 3)) * 8 + (quad & 7)) * 512 + val * 4);
+  };
+  const bool few = QPB == 4 && np <= kJoinAhead;
+  float4 first[kJoinAhead];
+#pragma unroll
+  for (int u = 0; u < kJoinAhead; ++u) {
+    const int k = few ? u : sub + 4 * u;
+    first[u] = k < np && (!few || sub < nq) ? at(few ? q0 + sub : q0, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int c = warp; c < 4 * nq; c += kJoinThreads / 32) {
+    // one warp: the weights of column 4 q0 + c in every piece
+    const int col = 4 * q0 + c;
+    float2 ml[kAttnMaxParts / 32];
     float top = -INFINITY;
-    if (col < n)
-      for (int k = lane; k < mt.y; k += 32) top = fmaxf(top, p.part_ml[slot_at(k) * kAttnCols + col].x);
+#pragma unroll
+    for (int u = 0; u < kAttnMaxParts / 32; ++u) {
+      const int k = lane + 32 * u;
+      ml[u] = col < n && k < np ? p.part_ml[slot_at(k) * kAttnCols + col] : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, ml[u].x);
+    }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     const float ref = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    if (col < n)
-      for (int k = lane; k < mt.y; k += 32) {
-        const float2 ml = p.part_ml[slot_at(k) * kAttnCols + col];
-        sum = fmaf(ml.y, exp2f(ml.x - ref), sum);
-      }
+#pragma unroll
+    for (int u = 0; u < kAttnMaxParts / 32; ++u) {
+      ml[u].x = exp2f(ml[u].x - ref);
+      sum = fmaf(ml[u].y, ml[u].x, sum);
+    }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int k = lane; k < mt.y; k += 32)
-      (&wt[k].x)[warp] = col < n ? exp2f(p.part_ml[slot_at(k) * kAttnCols + col].x - ref) * inv : 0.f;
-    if (vb == 0 && lane == 0 && p.lse && col < n) p.lse[oc + warp] = (top + log2f(sum)) * 0.69314718055994531f;
+#pragma unroll
+    for (int u = 0; u < kAttnMaxParts / 32; ++u)
+      if (lane + 32 * u < np) (&wt[lane + 32 * u][c >> 2].x)[c & 3] = ml[u].x * inv;
+    if (vb == 0 && lane == 0 && p.lse && col < n) p.lse[oc + col] = (top + log2f(sum)) * 0.69314718055994531f;
   }
   __syncthreads();
-  const float* src = p.part_o + ((vb * 2 + (quad >> 3)) * 8 + (quad & 7)) * 512 + tid * 4;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = 0; k < mt.y; ++k) {
-    const float4 v = *reinterpret_cast<const float4*>(src + slot_at(k) * (kAttnCols * kLatent));
-    const float4 w = wt[k];
+  float4 acc;
+  auto add = [&](const float4& v, const float4& w) {
     acc.x = fmaf(v.x, w.x, acc.x);
     acc.y = fmaf(v.y, w.y, acc.y);
     acc.z = fmaf(v.z, w.z, acc.z);
     acc.w = fmaf(v.w, w.w, acc.w);
-  }
+  };
+  auto write = [&](int quad) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (4 * quad + e < n)
-      p.out[(oc + e) * kLatent + vb * 128 + tid] = static_cast<uint16_t>(pack_bf16((&acc.x)[e], 0.f));
+    for (int e = 0; e < 4; ++e)
+      if (4 * quad + e < n)
+        p.out[(oc + 4 * quad + e) * kLatent + vb * 128 + val] = static_cast<uint16_t>(pack_bf16((&acc.x)[e], 0.f));
+  };
+  if (few) {
+    if (sub >= nq) return;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kJoinAhead; ++u)
+      if (u < np) add(first[u], wt[u][sub]);
+    write(q0 + sub);
+    return;
+  }
+  for (int q = 0; q < nq; ++q) {
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (q > 0) {
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u)
+        first[u] = sub + 4 * u < np ? at(q0 + q, sub + 4 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kJoinAhead; ++u)
+      if (sub + 4 * u < np) add(first[u], wt[sub + 4 * u][q]);
+#pragma unroll 4
+    for (int k = sub + 4 * kJoinAhead; k < np; k += 4) add(at(q0 + q, k), wt[k][q]);
+    if (sub > 0) acc_of[sub - 1][val] = acc;
+    __syncthreads();
+    if (sub == 0) {
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const float4 v = acc_of[u][val];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+      }
+      write(q0 + q);
+    }
+    __syncthreads();
+  }
 }
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, cudaStream_t st) {
@@ -1197,10 +1279,16 @@ cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, 
   void* args[] = {&copy};
   e = cudaLaunchKernelExC(&cfg, kern, args);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 64);  // four value blocks x 16 column quads
-  cfg.blockDim = dim3(128);
+  // four value blocks x column quads (all a block can hold, or one where few groups can be cut)
+  const int quads = (min(kAttnCols, p.R * p.H) + 3) / 4;
+  const bool spread = p.groups <= kSpreadGroups;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(4 * (spread ? quads : (quads + 3) / 4)));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(latent_combine_kernel), args);
+  return cudaLaunchKernelExC(&cfg,
+                             spread ? reinterpret_cast<const void*>(latent_combine_kernel<1>)
+                                    : reinterpret_cast<const void*>(latent_combine_kernel<4>),
+                             args);
 }
 
 }  // namespace fp8idx
