@@ -24,10 +24,9 @@
 //              the sums from TMEM, divide and write.
 //   warps 4-7  (fp8: 4-11) producers: gather the tile's key rows into one of
 //              two stages in the 128-byte swizzle.  bf16: 16-byte
-//              asynchronous copies.  fp8: two sets of four warps, each with
-//              every second tile: its codes wait in registers until the stage
-//              is free and become bf16 on the way into it, exactly; the
-//              scales go to the softmax warps.
+//              asynchronous copies.  fp8: the codes come one tile ahead into
+//              registers and become fp16 on the way into the stage, exactly;
+//              the scales go to the softmax warps.
 //   two more   one issues the score products, part by part as a tile lands,
 //   warps      the other the value products.
 // Scores: M = 64 columns, N = 64 keys, K = 576.  Values, transposed so that
@@ -50,15 +49,13 @@ constexpr int kChunkBytes = kAttnKeys * 128;    // [64 keys][64 values] bf16, sw
 constexpr int kStageBytes = kChunks * kChunkBytes;
 constexpr int kParts = 5;                       // barriers of a stage: four chunk pairs, and the rotated part
 constexpr int kInfo = 4;                        // tile descriptions in flight
-constexpr int kSet = 128;                       // threads that bring one tile
-
 // The kernel's shape for a kind of pool.
 template <bool FP8>
 struct Shape {
   static constexpr int kSwg = FP8 ? 1 : 2;        // softmax warpgroups, each with 64 / kSwg of a tile's keys
   static constexpr int kSoftmax = 128 * kSwg;
-  static constexpr int kSets = FP8 ? 2 : 1;       // producer sets
-  static constexpr int kThreads = kSoftmax + kSets * kSet + 64;
+  static constexpr int kProducers = FP8 ? 256 : 128;
+  static constexpr int kThreads = kSoftmax + kProducers + 64;
   static constexpr int kFull = FP8 ? 3 : 2;       // announcements of a tile's parts
   // the parts that announcement f covers
   __host__ __device__ static constexpr int first_part(int f) { return f == 0 ? 0 : f == 1 ? 2 : FP8 && f == 2 ? 4 : 5; }
@@ -287,7 +284,7 @@ __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kAttnKey
 template <bool PAGED, bool FP8>
 __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(const __grid_constant__ LatentAttnParams p) {
   using Sh = Shape<FP8>;
-  constexpr int kThreads = Sh::kThreads, kSoftmax = Sh::kSoftmax, kSwg = Sh::kSwg;
+  constexpr int kThreads = Sh::kThreads, kSoftmax = Sh::kSoftmax, kSwg = Sh::kSwg, kProducers = Sh::kProducers;
   constexpr int kScoreWarp = kThreads / 32 - 2, kValueWarp = kThreads / 32 - 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
@@ -300,10 +297,10 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     for (int s = 0; s < kStages; ++s)
       for (int i = 0; i < kParts; ++i) {
         // codes: one arrival a warp; asynchronous copies: one a thread (bf16: and one with the tile's description)
-        mbar_init(&ms.full[s][i], FP8 && i < 2 ? kSet / 32 : kSet + (i == 0 ? 1 : 0));
+        mbar_init(&ms.full[s][i], FP8 && i < 2 ? kProducers / 32 : kProducers + (!FP8 && i == 0 ? 1 : 0));
         mbar_init(&ms.empty[s][i], 1);
       }
-    mbar_init(&ms.q_full, kSet);
+    mbar_init(&ms.q_full, kProducers);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ms.s_full[b], 1);
       mbar_init(&ms.s_empty[b], kSoftmax);
@@ -377,8 +374,9 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 
   if (warp >= kSoftmax / 32 && warp < kScoreWarp) {
     // ================================================================ producers
-    const int set = (tid - kSoftmax) / kSet, pt = (tid - kSoftmax) % kSet;
-    const int piece = pt & 7, r0 = pt >> 3;  // 16-byte piece of a chunk row; rows r0 + 16 k
+    constexpr int kRows = kProducers / 8, NK = kAttnKeys / kRows;  // rows side by side, rows a thread
+    const int pt = tid - kSoftmax;
+    const int piece = pt & 7, r0 = pt >> 3;  // 16-byte piece of a chunk row; rows r0 + kRows k
     const uint32_t row_dst = smem_u32(smem + kOffK) + r0 * 128;
     const uint32_t swz = (piece ^ (r0 & 7)) << 4;
     // fp8: 16 codes become pieces 2 (piece % 4) and the next of chunk piece / 4;
@@ -395,9 +393,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     int left = static_cast<int>(x1 - x0);  // tiles of this CTA's range behind the current segment
     const int32_t* list = nullptr;
     int bad = 0;
-    // raw list entries of keys lane and lane + 32 (paged: the page) of the next
-    // tile, and (two sets) of the one after it
-    int next_idx[2] = {-1, -1}, then_idx[2] = {-1, -1};
+    int next_idx[2] = {-1, -1};         // raw list entries of its keys lane and lane + 32 (paged: the page)
     if (PAGED) {
       g = ms.start_group;
       t = ms.start_tile;
@@ -413,7 +409,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       te = min(nt, t + left);
       direct = t == 0 && te == nt;
       fresh = true;
-      if (t == 0 && te < nt && set == 0 && pt == 0) {
+      if (t == 0 && te < nt && pt == 0) {
         // the group goes on in the ranges after this one, up to the one that holds its last tile
         const int64_t last = x1 - left + nt - 1;
         const int c1 = static_cast<int>(((last + 1) * parts - 1) / total);
@@ -424,37 +420,24 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
                    : p.slots + static_cast<int64_t>(g) * p.ld_slots;
       left -= te - t;
     };
-    auto fetch_idx = [&](int tt, int (&to)[2]) {
+    auto fetch_idx = [&]() {
       if (PAGED) {
-        to[0] = tt < te && tt * kAttnKeys < len ? __ldg(list + tt) : -1;  // a tile is a page
+        next_idx[0] = t < te && t * kAttnKeys < len ? __ldg(list + t) : -1;  // a tile is a page
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int j = tt * kAttnKeys + h * 32 + lane;
-          to[h] = tt < te && j < len ? __ldg(list + j) : -1;
+          const int j = t * kAttnKeys + h * 32 + lane;
+          next_idx[h] = t < te && j < len ? __ldg(list + j) : -1;
         }
-      }
-    };
-    auto first_idx = [&]() {
-      fetch_idx(t, next_idx);
-      if (FP8) fetch_idx(t + 1, then_idx);
-    };
-    auto shift_idx = [&]() {
-      if (FP8) {
-        next_idx[0] = then_idx[0];
-        next_idx[1] = then_idx[1];
-        fetch_idx(t + 1, then_idx);
-      } else {
-        fetch_idx(t, next_idx);
       }
     };
 
     // ---- the tile about to be written (fp8: its rows on the way in registers)
     Info d;
-    uint4 raw[FP8 ? 16 : 1];
+    uint4 raw[FP8 ? 4 * NK : 1];
     float sc = 0.f;
-    int row[4];              // pool slots of its rows r0 + 16 k, -1 where there is none
-    const uint8_t* src[4];   // bf16: their addresses
+    int row[NK];             // pool slots of its rows r0 + kRows k, -1 where there is none
+    const uint8_t* src[NK];  // their addresses
     const int num_slots = static_cast<int>(p.num_slots), num_pages = num_slots / kPageSize;
     // Finds the next tile that holds keys (or ends a segment, or the stream) and describes it in d.
     auto advance = [&]() {
@@ -467,7 +450,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           ++g;
           t = 0;
           open_segment();
-          first_idx();
+          fetch_idx();
         }
         int sl[2];
 #pragma unroll
@@ -496,14 +479,14 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         d.ends = PAGED ? len - p.R + 1 - t * kAttnKeys : 1 << 20;
         d.piece = static_cast<int>(blockIdx.x) * 2 + (from_start ? 1 : 0);
         ++t;
-        shift_idx();
+        fetch_idx();
         if (null && !last) continue;  // nothing to do and nothing to say
         if (!null) {
           fresh = false;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            row[k] = __shfl_sync(0xFFFFFFFFu, sl[k >> 1], (r0 + 16 * k) & 31);
-            if (!FP8) src[k] = p.kv + static_cast<int64_t>(max(row[k], 0)) * kRowBytes + piece * 16;
+          for (int k = 0; k < NK; ++k) {
+            row[k] = __shfl_sync(0xFFFFFFFFu, sl[kRows * k >> 5], (r0 + kRows * k) & 31);
+            src[k] = p.kv + static_cast<int64_t>(max(row[k], 0)) * kRowBytes + piece * 16;
           }
           if (FP8 && pt < kAttnKeys) {
             const int v = pt < 32 ? sl[0] : sl[1];
@@ -513,22 +496,17 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         return;
       }
     };
-    // fp8: the tile's codes (16 bytes of part c in raw[4 c + k]).
-    auto load_raw = [&]() {
-      if (FP8) {
+    // fp8: the codes of part c, 16 bytes a row, into registers; and from there, as fp16, into the stage.
+    auto load_part = [&](int c) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint8_t* at = p.kv + static_cast<int64_t>(max(row[k], 0)) * kLatent + piece * 16;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) raw[4 * c + k] = row[k] >= 0 ? ld_stream16(at + c * 128) : make_uint4(0, 0, 0, 0);
-        }
-      }
+      for (int k = 0; k < NK; ++k)
+        raw[FP8 ? NK * c + k : 0] = row[k] >= 0 ? ld_stream16(src[k] + c * 128) : make_uint4(0, 0, 0, 0);
     };
     auto store_part = [&](int c, uint32_t dst) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t rd = dst + k * 2048 + 2 * c * kChunkBytes;
-        const uint4 v = raw[FP8 ? 4 * c + k : 0];
+      for (int k = 0; k < NK; ++k) {
+        const uint32_t rd = dst + k * (kRows * 128) + 2 * c * kChunkBytes;
+        const uint4 v = raw[FP8 ? NK * c + k : 0];
         uint32_t a[4], b[4];
         e4m3x4_f16(v.x, a[0], a[1]);
         e4m3x4_f16(v.y, a[2], a[3]);
@@ -543,13 +521,13 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     auto copy_q = [&](int group) {
       const int cols = p.R * p.H;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int col = cg * kAttnCols + r0 + 16 * k;
+      for (int k = 0; k < NK; ++k) {
+        const int col = cg * kAttnCols + r0 + kRows * k;
         const bool v = col < cols;
         const int qr = PAGED && v ? col / p.H : 0, h = v ? col - qr * p.H : 0;
         const uint8_t* qs = reinterpret_cast<const uint8_t*>(
             p.q + (static_cast<int64_t>(group) * p.R + qr) * p.q_row + h * p.q_head) + piece * 16;
-        const uint32_t qd = smem_u32(smem + kOffQ) + (r0 + 16 * k) * 128 + swz;
+        const uint32_t qd = smem_u32(smem + kOffQ) + (r0 + kRows * k) * 128 + swz;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) cp_async16(qd + c * kChunkBytes, qs + c * 128, v ? 16 : 0);
       }
@@ -559,11 +537,11 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     // next to 2^14: exact but for values 2^28 times smaller, whose error
     // (2^-39 of the largest) is below the fp32 sum's.  The rotated part meets
     // bf16 and stays bf16.  A thread converts the pieces that it copied.
-    auto convert_q = [&](float (&fac)[4]) {
+    auto convert_q = [&](float (&fac)[NK]) {
       cp_async_wait_all();
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        uint8_t* at = smem + kOffQ + (r0 + 16 * k) * 128 + swz;
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        uint8_t* at = smem + kOffQ + (r0 + kRows * k) * 128 + swz;
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
@@ -596,41 +574,35 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           *reinterpret_cast<uint4*>(at + c * kChunkBytes) = v;
         }
       }
-      fence_async_shared();
       mbar_arrive(&ms.q_full);
     };
 
     bool ok = true;
     if (left > 0) {
       open_segment();
-      first_idx();
+      fetch_idx();
       // on its way while the first list entries are; used if tile 0 holds keys (it is then of this group)
-      if (set == 0) copy_q(g);
+      copy_q(g);
     } else {
       t = te;
     }
     advance();
-    if (FP8 && set == 1) {
-      if (d.flags & kEnd) ok = false;  // set 0 announces the end
-      else advance();
+    if (FP8 && !(d.flags & (kNull | kEnd))) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) load_part(c);
     }
-    if (FP8 && ok && !(d.flags & (kNull | kEnd))) load_raw();
-    for (int i = set; ok; i += FP8 ? 2 : 1) {
+    for (int i = 0; ok; ++i) {
       const int st = i & 1;
       const uint32_t ph = (i >> 1) & 1;
       const int flags = d.flags;
       const bool null = flags & (kNull | kEnd);
       if ((flags & kFirst) && !null && i > 0) {
-        // ---- the group's query columns; their place is free once the scores
-        // of tile i - 1 are done.  Tile i - 2's first: only then is the other
-        // barrier's phase the one asked for or the one before it (a set sees
-        // every second tile alone).
-        if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit)) break;
+        // ---- the group's query columns; their place is free once the scores of tile i - 1 are done
         if (!warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) break;
         copy_q(d.group);
       }
       if (i == 0 && null) cp_async_wait_all();  // the queries copied ahead are not used: out of the way of the next ones
-      float qfac[4];
+      float qfac[NK];
       if ((flags & kFirst) && !null) {
         if (FP8) convert_q(qfac);
         else cp_async_arrive(&ms.q_full);
@@ -651,7 +623,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
       if (FP8 && (flags & kFirst) && !null && piece == 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ms.q_scale[st][r0 + 16 * k] = qfac[k];
+        for (int k = 0; k < NK; ++k) ms.q_scale[st][r0 + kRows * k] = qfac[k];
       }
       const bool withhold = p.debug_withhold_first_tile && i == 0;
       const uint32_t dst = row_dst + st * kStageBytes;
@@ -659,8 +631,8 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         // the rotated part, bf16 as it is: asynchronous copies, on their way while the codes are converted
         if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit)) break;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          cp_async16(dst + 8 * kChunkBytes + k * 2048 + swz,
+        for (int k = 0; k < NK; ++k)
+          cp_async16(dst + 8 * kChunkBytes + k * (kRows * 128) + swz,
                      p.pe + static_cast<int64_t>(max(row[k], 0)) * (kRope * 2) + piece * 16, row[k] >= 0 ? 16 : 0);
         cp_async_arrive(&ms.full[st][2]);
       }
@@ -671,21 +643,19 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         for (int c = Sh::first_part(f); c < Sh::first_part(f + 1); ++c) {
           if (c > 0 && !(flags & kEnd) &&
               !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
-          if (null) continue;
           if (FP8) {
-            if (c < 4) store_part(c, dst);
-          } else {
+            if (c < 4 && !null) store_part(c, dst);
+          } else if (!null) {
 #pragma unroll
             for (int u = 0; u < (c < 4 ? 2 : 1); ++u)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                cp_async16(dst + (2 * c + u) * kChunkBytes + k * 2048 + swz, src[k] + (2 * c + u) * 128,
+              for (int k = 0; k < NK; ++k)
+                cp_async16(dst + (2 * c + u) * kChunkBytes + k * (kRows * 128) + swz, src[k] + (2 * c + u) * 128,
                            row[k] >= 0 ? 16 : 0);
           }
         }
         if (!ok) break;
         if (FP8 && f < 2) {
-          fence_async_shared();
           __syncwarp();
           if (lane == 0 && !(withhold && f == 0)) mbar_arrive(&ms.full[st][f]);
         } else if (FP8 && !null) {
@@ -698,12 +668,13 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
       if (!ok) break;
       if (flags & kEnd) break;
-      // ---- the next tile (fp8: of this set; its loads go out now, with no fence behind them until they are used)
       advance();
-      if (FP8) {
-        if (d.flags & kEnd) break;  // the other set announces it
-        advance();
-        if (!(d.flags & (kNull | kEnd))) load_raw();
+      // fp8: the next tile's codes, all at once and behind the last use of this
+      // one's: a wait for a register filled by an earlier load would also wait
+      // for loads issued since
+      if (FP8 && !(d.flags & (kNull | kEnd))) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) load_part(c);
       }
     }
     cp_async_wait_all();
@@ -739,13 +710,14 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       if (flags & kFirst) {
         if (!warp_wait(&ms.q_full, nq & 1, abort_flag, &ms.status, limit)) break;
         ++nq;
-        if (!FP8) fence_async_shared();  // the queries came by asynchronous copies of other threads
+        fence_async_shared();  // other threads wrote the queries
       }
       bool ok = true;
 #pragma unroll
       for (int f = 0; f < Sh::kFull; ++f) {
         if (f > 0 && !warp_wait(&ms.full[st][f], ph, abort_flag, &ms.status, limit)) { ok = false; break; }
-        if (!FP8 || f == 2) fence_async_shared();  // these rows came by asynchronous copies of other threads
+        // the rows were written by other threads
+        fence_async_shared();
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
