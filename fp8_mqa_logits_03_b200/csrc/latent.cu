@@ -22,7 +22,7 @@
 //              four lanes a head), running maximum and sum in registers,
 //              weights as bf16 into shared memory; at a group's end they read
 //              the sums from TMEM, divide and write.
-//   warps 4-7  (fp8: 4-11) producers: gather the tile's key rows into one of
+//   four warps producers: gather the tile's key rows into one of
 //              two stages in the 128-byte swizzle.  bf16: 16-byte
 //              asynchronous copies.  fp8: the codes come one tile ahead into
 //              registers and become fp16 on the way into the stage, exactly;
@@ -54,7 +54,7 @@ template <bool FP8>
 struct Shape {
   static constexpr int kSwg = FP8 ? 1 : 2;        // softmax warpgroups, each with 64 / kSwg of a tile's keys
   static constexpr int kSoftmax = 128 * kSwg;
-  static constexpr int kProducers = FP8 ? 256 : 128;
+  static constexpr int kProducers = 128;
   static constexpr int kThreads = kSoftmax + kProducers + 64;
   static constexpr int kFull = FP8 ? 3 : 2;       // announcements of a tile's parts
   // the parts that announcement f covers
@@ -177,15 +177,22 @@ __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 32 lanes x 16 consecutive columns, one lane a thread.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -240,6 +247,14 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_u32x2(uint64_t v, uint32_t& lo, uint32_t& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -437,7 +452,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     uint4 raw[FP8 ? 4 * NK : 1];
     float sc = 0.f;
     int row[NK];             // pool slots of its rows r0 + kRows k, -1 where there is none
-    const uint8_t* src[NK];  // their addresses
     const int num_slots = static_cast<int>(p.num_slots), num_pages = num_slots / kPageSize;
     // Finds the next tile that holds keys (or ends a segment, or the stream) and describes it in d.
     auto advance = [&]() {
@@ -486,7 +500,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 #pragma unroll
           for (int k = 0; k < NK; ++k) {
             row[k] = __shfl_sync(0xFFFFFFFFu, sl[kRows * k >> 5], (r0 + kRows * k) & 31);
-            src[k] = p.kv + static_cast<int64_t>(max(row[k], 0)) * kRowBytes + piece * 16;
           }
           if (FP8 && pt < kAttnKeys) {
             const int v = pt < 32 ? sl[0] : sl[1];
@@ -497,10 +510,11 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
     };
     // fp8: the codes of part c, 16 bytes a row, into registers; and from there, as fp16, into the stage.
+    auto row_at = [&](int v) { return p.kv + static_cast<int64_t>(max(v, 0)) * kRowBytes + piece * 16; };
     auto load_part = [&](int c) {
 #pragma unroll
       for (int k = 0; k < NK; ++k)
-        raw[FP8 ? NK * c + k : 0] = row[k] >= 0 ? ld_stream16(src[k] + c * 128) : make_uint4(0, 0, 0, 0);
+        raw[FP8 ? NK * c + k : 0] = row[k] >= 0 ? ld_stream16(row_at(row[k]) + c * 128) : make_uint4(0, 0, 0, 0);
     };
     auto store_part = [&](int c, uint32_t dst) {
 #pragma unroll
@@ -650,7 +664,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
             for (int u = 0; u < (c < 4 ? 2 : 1); ++u)
 #pragma unroll
               for (int k = 0; k < NK; ++k)
-                cp_async16(dst + (2 * c + u) * kChunkBytes + k * (kRows * 128) + swz, src[k] + (2 * c + u) * 128,
+                cp_async16(dst + (2 * c + u) * kChunkBytes + k * (kRows * 128) + swz, row_at(row[k]) + (2 * c + u) * 128,
                            row[k] >= 0 ? 16 : 0);
           }
         }
@@ -809,87 +823,62 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
       uint32_t w[2 * NJ], r[NR];
       float mx[2] = {-INFINITY, -INFINITY}, la[2];
-      // The weights of this thread's keys, with the reference maxima as they are, and their sums.
-      auto weigh = [&]() {
-        float neg[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          neg[h] = m[h] == -INFINITY ? 0.f : -m[h];
-          la[h] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          float2 inv;
-          if (FP8) inv = *reinterpret_cast<const float2*>(&ms.scale[b][2][8 * j + cq]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float x = __uint_as_float(r[4 * j + 2 * h]), y = __uint_as_float(r[4 * j + 2 * h + 1]);
-            if (FP8) {
-              const float a = ex2(x + neg[h]), c = ex2(y + neg[h]);
-              // (an unseen key's scale may be anything)
-              la[h] = a == 0.f ? la[h] : fmaf(a, inv.x, la[h]);
-              la[h] = c == 0.f ? la[h] : fmaf(c, inv.y, la[h]);
-              w[2 * j + h] = pack_f16(a, c);
-            } else {
-              const float a = ex2(fmaf(x, to_log2[h], neg[h])), c = ex2(fmaf(y, to_log2[h], neg[h]));
-              la[h] += a + c;
-              w[2 * j + h] = pack_bf16(a, c);
-            }
-          }
-        }
-      };
-      auto put_weights = [&]() {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          *reinterpret_cast<uint32_t*>(prow + (((wg * NJ + j) ^ (rr & 7)) << 4)) = w[2 * j];
-          *reinterpret_cast<uint32_t*>(prow + 8 * 128 + (((wg * NJ + j) ^ (rr & 7)) << 4)) = w[2 * j + 1];
-        }
-      };
-      bool grow = false;
-      const bool live = !(flags & (kNull | kEnd));
-      if (live) {
+      bool poison = false;  // fp8: a key that a row must not see has a scale that is not finite
+      // The tile's scores (fp8: in log2 units, with the keys' scales), unseen ones -inf, and this thread's maxima.
+      auto read_scores = [&]() {
         tmem_ld_16(tbase + kTmemS + b * 64 + wg * kKeys + lane_base, r);
         if (FP8) {
-          uint32_t e[NR];
-          tmem_ld_16(tbase + kTmemPe + b * 64 + wg * kKeys + lane_base, e);
-          tmem_ld_wait();
           // (codes . q) s + rotated part, in log2 units, plus log2 s: the
           // weight of key j is exp2 of this, i.e. it carries the key's scale
+          const uint64_t tl2[2] = {pack_f32x2(to_log2[0], to_log2[0]), pack_f32x2(to_log2[1], to_log2[1])};
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const float2 v = *reinterpret_cast<const float2*>(&ms.scale[b][0][8 * j + cq]);
-            const float2 g = *reinterpret_cast<const float2*>(&ms.scale[b][1][8 * j + cq]);
+          for (int half = 0; half < NJ / 4; ++half) {  // 32 columns at a time
+            uint32_t e[16];
+            tmem_ld_16(tbase + kTmemPe + b * 64 + half * 32 + lane_base, e);
+            tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int x = 4 * j + 2 * h;
-              r[x] = __float_as_uint(
-                  fmaf(fmaf(__uint_as_float(r[x]), v.x, __uint_as_float(e[x])), to_log2[h], g.x));
-              r[x + 1] = __float_as_uint(
-                  fmaf(fmaf(__uint_as_float(r[x + 1]), v.y, __uint_as_float(e[x + 1])), to_log2[h], g.y));
+            for (int jj = 0; jj < 4; ++jj) {
+              const int j = half * 4 + jj;
+              const uint64_t v2 = *reinterpret_cast<const uint64_t*>(&ms.scale[b][0][8 * j + cq]);
+              const uint64_t g2 = *reinterpret_cast<const uint64_t*>(&ms.scale[b][1][8 * j + cq]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int x = 4 * j + 2 * h, y = 4 * jj + 2 * h;
+                uint64_t z = fma_f32x2(pack_u32x2(r[x], r[x + 1]), v2, pack_u32x2(e[y], e[y + 1]));
+                z = fma_f32x2(z, tl2[h], g2);
+                unpack_u32x2(z, r[x], r[x + 1]);
+              }
             }
           }
         } else {
           tmem_ld_wait();
         }
-        tc_fence_before();
-        mbar_arrive(&ms.s_empty[b]);
         const unsigned long long mask = f.mask;
         const int ends = f.ends;
+        mx[0] = mx[1] = -INFINITY;
         const bool whole = mask == ~0ull && ends >= kAttnKeys;
         if (!whole) {
+          // bit 8 j + e: key 8 j + cq + e exists, and row h sees it
+          const unsigned long long here = mask >> cq;
+          unsigned long long sees[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int lim = ends + trow[h];  // keys of the tile that the row sees
+            sees[h] = (lim >= kAttnKeys ? mask : lim <= 0 ? 0ull : mask & ((1ull << lim) - 1)) >> cq;
+          }
 #pragma unroll
           for (int j = 0; j < NR; ++j) {
-            const int key = 8 * (j >> 2) + cq + (j & 1), h = (j >> 1) & 1;
-            const bool real = (mask >> key) & 1;
-            const bool seen = real && key < ends + trow[h];
+            const int h = (j >> 1) & 1, bit = 8 * (j >> 2) + (j & 1);
+            const bool real = (here >> bit) & 1, seen = (sees[h] >> bit) & 1;
             if (PAGED && real && !seen && !(fabsf(__uint_as_float(r[j])) < INFINITY)) {
               // a key that this row must not see is not finite: 0 * value would
               // not be 0, so its values become 0 (rows that see it have a
               // score that is not finite, and keep it)
-              uint8_t* krow = smem + kOffK + b * kStageBytes + key * 128;
+              uint8_t* krow = smem + kOffK + b * kStageBytes + (bit + cq) * 128;
               for (int c = 0; c < 8; ++c)
                 for (int x = 0; x < 8; ++x)
                   *reinterpret_cast<uint4*>(krow + c * kChunkBytes + x * 16) = make_uint4(0, 0, 0, 0);
+              poison = true;
             }
             if (!seen) r[j] = 0xFF800000u;
           }
@@ -900,70 +889,132 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           mx[1] = fmaxf(mx[1], fmaxf(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
         }
 #pragma unroll
+        for (int h = 0; h < 2; ++h) mx[h] = (FP8 ? mx[h] : mx[h] * to_log2[h]) - kBias;
+      };
+      // The weights of this thread's keys, with the reference maxima as they
+      // are, and their sums (packed pairs of keys).
+      auto weigh = [&]() {
+        uint64_t neg2[2], la2[2] = {0, 0}, tl2[2];
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mx[h] = (FP8 ? mx[h] : mx[h] * to_log2[h]) - kBias;
-          grow = grow || mx[h] > m[h] + kRescaleLog2;
+          const float neg = m[h] == -INFINITY ? 0.f : -m[h];
+          neg2[h] = pack_f32x2(neg, neg);
+          tl2[h] = pack_f32x2(to_log2[h], to_log2[h]);
         }
-        if (!(flags & kFirst)) weigh();
-      } else if (!end && !dead) {
-        mbar_arrive(&ms.s_empty[b]);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          uint64_t inv2;
+          if (FP8) inv2 = *reinterpret_cast<const uint64_t*>(&ms.scale[b][2][8 * j + cq]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t x2 = pack_u32x2(r[4 * j + 2 * h], r[4 * j + 2 * h + 1]);
+            float a, c;
+            unpack_f32x2(FP8 ? add_f32x2(x2, neg2[h]) : fma_f32x2(x2, tl2[h], neg2[h]), a, c);
+            a = ex2(a);
+            c = ex2(c);
+            la2[h] = FP8 ? fma_f32x2(pack_f32x2(a, c), inv2, la2[h]) : add_f32x2(pack_f32x2(a, c), la2[h]);
+            w[2 * j + h] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float a, c;
+          unpack_f32x2(la2[h], a, c);
+          la[h] = a + c;
+        }
+        if (FP8 && PAGED && poison) {  // 0 * (1 / scale) is not 0 there: the sums again, without such keys
+          la[0] = la[1] = 0.f;
+#pragma unroll
+          for (int j = 0; j < NR; ++j) {
+            float a, c;
+            unpack_f32x2(neg2[(j >> 1) & 1], a, c);
+            a = ex2(__uint_as_float(r[j]) + a);
+            if (a != 0.f) la[(j >> 1) & 1] += a * ms.scale[b][2][8 * (j >> 2) + cq + (j & 1)];
+          }
+        }
+      };
+      auto put_weights = [&]() {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          *reinterpret_cast<uint32_t*>(prow + (((wg * NJ + j) ^ (rr & 7)) << 4)) = w[2 * j];
+          *reinterpret_cast<uint32_t*>(prow + 8 * 128 + (((wg * NJ + j) ^ (rr & 7)) << 4)) = w[2 * j + 1];
+        }
+      };
+      const bool live = !(flags & (kNull | kEnd));
+      // Pass 0: the weights with the maxima as they are (not on a segment's
+      // first tile, which has none), and one vote: whether some score outgrew
+      // its column's reference maximum, the end, a wait that gave up.  Mostly
+      // none did, and the weights stand.  Else pass 1: new maxima, the sums so
+      // far scaled to them, and the weights again.
+      // (Pass 1 reads the scores once more: kept over the vote, they would spill.)
+      bool leave = false;
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (live && (pass == 1 || !(flags & kFirst))) read_scores();
+        if (pass == 1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
+          }
+          if (kSwg > 1) {
+            if ((lane & 3) == 0) {
+              ms.half_max[b][wg][rr] = mx[0];
+              ms.half_max[b][wg][rr + 8] = mx[1];
+            }
+            named_bar_sync(2, kSoftmax);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (kSwg > 1) mx[h] = fmaxf(mx[h], ms.half_max[b][wg ^ 1][rr + 8 * h]);
+            float fac = 1.f;
+            if (flags & kFirst) {
+              m[h] = mx[h];
+            } else if (mx[h] > m[h] + kRescaleLog2) {
+              fac = ex2(m[h] - mx[h]);
+              m[h] = mx[h];
+              l[h] *= fac;
+            }
+            if ((lane & 3) == 0 && wg == 0) ms.stat_m[rr + 8 * h] = fac;
+          }
+          if (!(flags & kFirst)) {
+            named_bar_sync(2, kSoftmax);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = wg; c < 16; c += kSwg) {
+              uint32_t o[16];
+              tmem_ld_x16(tbase + kTmemO + c * 16 + lane_base, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * ms.stat_m[(c & 3) * 16 + k]);
+              tmem_st_x16(tbase + kTmemO + c * 16 + lane_base, o);
+            }
+            tmem_st_wait();
+          }
+          named_bar_sync(2, kSoftmax);  // the factors are read before they are written again
+        }
+        const bool weighs = live && (pass == 1 || !(flags & kFirst));
+        if (weighs) weigh();
+        // the previous value product is done: the weights' buffer is free and the sums hold still
+        if (pass == 0 && i > 0 && !warp_wait(&ms.pv_done, (i - 1) & 1, abort_flag, &ms.status, limit)) dead = true;
+        if (weighs) put_weights();
+        if (pass == 1) break;
+        const bool grow = mx[0] > m[0] + kRescaleLog2 || mx[1] > m[1] + kRescaleLog2;
+        const bool vote = bar_red_or(1, kSoftmax, dead || end || grow);
+        if (vote && bar_red_or(1, kSoftmax, dead || end)) {
+          leave = true;
+          break;
+        }
+        if (!live || !(vote || (flags & kFirst))) break;
       }
-      // the previous value product is done: the weights' buffer is free and the sums hold still
-      if (i > 0 && !warp_wait(&ms.pv_done, (i - 1) & 1, abort_flag, &ms.status, limit)) dead = true;
-      if (live && !(flags & kFirst)) put_weights();
-      // One vote: whether some score outgrew its column's reference maximum,
-      // the end, a wait that gave up.  Mostly none did, and the weights taken
-      // with the old maximum stand.
-      const bool vote = bar_red_or(1, kSoftmax, dead || end || grow);
-      if (vote && bar_red_or(1, kSoftmax, dead || end)) {
+      if (leave) {
         mbar_arrive(&ms.p_full);  // the value warp sees the end too
         break;
       }
-      if (live && (vote || (flags & kFirst))) {
-        // ---- new maxima, and the sums so far scaled to them
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
-        }
-        if (kSwg > 1) {
-          if ((lane & 3) == 0) {
-            ms.half_max[b][wg][rr] = mx[0];
-            ms.half_max[b][wg][rr + 8] = mx[1];
-          }
-          named_bar_sync(2, kSoftmax);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (kSwg > 1) mx[h] = fmaxf(mx[h], ms.half_max[b][wg ^ 1][rr + 8 * h]);
-          float fac = 1.f;
-          if (flags & kFirst) {
-            m[h] = mx[h];
-          } else if (mx[h] > m[h] + kRescaleLog2) {
-            fac = ex2(m[h] - mx[h]);
-            m[h] = mx[h];
-            l[h] *= fac;
-          }
-          if ((lane & 3) == 0 && wg == 0) ms.stat_m[rr + 8 * h] = fac;
-        }
-        weigh();
-        put_weights();
-        if (!(flags & kFirst)) {
-          named_bar_sync(2, kSoftmax);
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = wg; c < 8; c += kSwg) {
-            uint32_t o[32];
-            tmem_ld32(tbase + kTmemO + c * 32 + lane_base, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              o[k] = __float_as_uint(__uint_as_float(o[k]) * ms.stat_m[(c & 1) * 32 + k]);
-            tmem_st32(tbase + kTmemO + c * 32 + lane_base, o);
-          }
-          tmem_st_wait();
-        }
-        named_bar_sync(2, kSoftmax);  // the factors are read before they are written again
+      if (!dead) {
+        tc_fence_before();
+        mbar_arrive(&ms.s_empty[b]);
       }
       if (live) {
         l[0] += la[0];
@@ -1005,9 +1056,10 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         // 16 values x this warpgroup's columns at a time: divided, rounded,
         // transposed through the warp's part of the weights' buffer, and
         // written as 16-byte pieces (8 values of one column)
-        constexpr int NC = kAttnCols / kSwg;
-        const int cb = wg * NC;
-        if (cb < n) {
+        // (32 columns: twice as many would spill)
+        constexpr int NC = 32;
+#pragma unroll 1
+        for (int cb = wg * NC; cb < n; cb += kSwg * NC) {
           float inv[NC / 4];
 #pragma unroll
           for (int j = 0; j < NC / 8; ++j) {
