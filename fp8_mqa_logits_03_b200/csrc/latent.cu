@@ -24,9 +24,9 @@
 //              the sums from TMEM, divide and write.
 //   four warps producers: gather the tile's key rows into one of
 //              two stages in the 128-byte swizzle.  bf16: 16-byte
-//              asynchronous copies.  fp8: the codes come one tile ahead into
-//              registers and become fp16 on the way into the stage, exactly;
-//              the scales go to the softmax warps.
+//              asynchronous copies.  fp8: the codes land in one half of the
+//              stage and become fp16 in its whole, exactly; the scales go to
+//              the softmax warps.
 //   two more   one issues the score products, part by part as a tile lands,
 //   warps      the other the value products.
 // Scores: M = 64 columns, N = 64 keys, K = 576.  Values, transposed so that
@@ -52,13 +52,14 @@ constexpr int kInfo = 4;                        // tile descriptions in flight
 // The kernel's shape for a kind of pool.
 template <bool FP8>
 struct Shape {
-  static constexpr int kSwg = FP8 ? 1 : 2;        // softmax warpgroups, each with 64 / kSwg of a tile's keys
+  static constexpr int kSwg = 2;                  // softmax warpgroups, each with 64 / kSwg of a tile's keys
   static constexpr int kSoftmax = 128 * kSwg;
   static constexpr int kProducers = 128;
   static constexpr int kThreads = kSoftmax + kProducers + 64;
   static constexpr int kFull = FP8 ? 3 : 2;       // announcements of a tile's parts
-  // the parts that announcement f covers
-  __host__ __device__ static constexpr int first_part(int f) { return f == 0 ? 0 : f == 1 ? 2 : FP8 && f == 2 ? 4 : 5; }
+  // the parts that announcement f covers (fp8: the second half's first)
+  __host__ __device__ static constexpr int first_part(int f) { return FP8 ? (f == 0 ? 2 : f == 1 ? 0 : f == 2 ? 4 : 5) : (f == 0 ? 0 : f == 1 ? 2 : 5); }
+  __host__ __device__ static constexpr int end_part(int f) { return FP8 ? (f == 0 ? 4 : f == 1 ? 2 : 5) : (f == 0 ? 2 : 5); }
 };
 constexpr int kMaxThreads = 448;
 static_assert(Shape<true>::kThreads <= kMaxThreads && Shape<false>::kThreads <= kMaxThreads, "threads");
@@ -99,16 +100,8 @@ struct Misc {
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full, pv_done, drain;
   Info info[kInfo];
-  union {
-    struct {
-      float scale[2][3][kAttnKeys];  // fp8: the tile's key scales s, log2 s and 1 / s, by tile parity
-      float q_scale[2][kAttnCols];   // fp8: what a column's scores are multiplied by (log2 units)
-    };
-    struct {
-      float half_max[2][2][kAttnCols];  // two softmax warpgroups: their keys' maxima, by tile parity
-      float stat_l1[kAttnCols];         // and the second one's sums
-    };
-  };
+  float scale[2][3][kAttnKeys];  // fp8: the tile's key scales s, log2 s and 1 / s, by tile parity
+  float q_scale[2][kAttnCols];   // fp8: what a column's scores are multiplied by (log2 units)
   float stat_m[kAttnCols], stat_l[kAttnCols];
   uint32_t tmem;
   int abort_flag;
@@ -212,11 +205,12 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // (tensor core) reads of the same shared memory.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(reinterpret_cast<uint64_t>(p)));
+               : "r"(src)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -447,9 +441,8 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
     };
 
-    // ---- the tile about to be written (fp8: its rows on the way in registers)
+    // ---- the tile about to be written
     Info d;
-    uint4 raw[FP8 ? 4 * NK : 1];
     float sc = 0.f;
     int row[NK];             // pool slots of its rows r0 + kRows k, -1 where there is none
     const int num_slots = static_cast<int>(p.num_slots), num_pages = num_slots / kPageSize;
@@ -509,26 +502,17 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         return;
       }
     };
-    // fp8: the codes of part c, 16 bytes a row, into registers; and from there, as fp16, into the stage.
     auto row_at = [&](int v) { return p.kv + static_cast<int64_t>(max(v, 0)) * kRowBytes + piece * 16; };
-    auto load_part = [&](int c) {
-#pragma unroll
-      for (int k = 0; k < NK; ++k)
-        raw[FP8 ? NK * c + k : 0] = row[k] >= 0 ? ld_stream16(row_at(row[k]) + c * 128) : make_uint4(0, 0, 0, 0);
-    };
-    auto store_part = [&](int c, uint32_t dst) {
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        const uint32_t rd = dst + k * (kRows * 128) + 2 * c * kChunkBytes;
-        const uint4 v = raw[FP8 ? NK * c + k : 0];
-        uint32_t a[4], b[4];
-        e4m3x4_f16(v.x, a[0], a[1]);
-        e4m3x4_f16(v.y, a[2], a[3]);
-        e4m3x4_f16(v.z, b[0], b[1]);
-        e4m3x4_f16(v.w, b[2], b[3]);
-        st_shared16(rd + fdst0, odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? b[2] : a[2], odd ? b[3] : a[3]);
-        st_shared16(rd + fdst1, odd ? a[0] : b[0], odd ? a[1] : b[1], odd ? a[2] : b[2], odd ? a[3] : b[3]);
-      }
+    // fp8: 16 codes of part c, row r0 + kRows k, into the stage as fp16.
+    auto store_codes = [&](const uint4& v, int c, int k, uint32_t dst) {
+      const uint32_t rd = dst + k * (kRows * 128) + 2 * c * kChunkBytes;
+      uint32_t a[4], b[4];
+      e4m3x4_f16(v.x, a[0], a[1]);
+      e4m3x4_f16(v.y, a[2], a[3]);
+      e4m3x4_f16(v.z, b[0], b[1]);
+      e4m3x4_f16(v.w, b[2], b[3]);
+      st_shared16(rd + fdst0, odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? b[2] : a[2], odd ? b[3] : a[3]);
+      st_shared16(rd + fdst1, odd ? a[0] : b[0], odd ? a[1] : b[1], odd ? a[2] : b[2], odd ? a[3] : b[3]);
     };
 
     // ---- the group's query columns
@@ -601,10 +585,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       t = te;
     }
     advance();
-    if (FP8 && !(d.flags & (kNull | kEnd))) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) load_part(c);
-    }
     for (int i = 0; ok; ++i) {
       const int st = i & 1;
       const uint32_t ph = (i >> 1) & 1;
@@ -642,24 +622,65 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const bool withhold = p.debug_withhold_first_tile && i == 0;
       const uint32_t dst = row_dst + st * kStageBytes;
       if (FP8 && !null) {
-        // the rotated part, bf16 as it is: asynchronous copies, on their way while the codes are converted
+        // The codes land in the first half of the stage, and the rotated part,
+        // bf16 as it is, in its place.  The second half's codes become fp16 in
+        // the second half; then every thread takes the others that it copied
+        // into registers, and when all have, they become fp16 in the first.
+        if (!warp_wait(&ms.empty[st][1], ph ^ 1, abort_flag, &ms.status, limit)) break;
+        const uint32_t land = dst + swz;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < NK; ++k)
+            cp_async16(land + c * kChunkBytes + k * (kRows * 128), row_at(row[k]) + c * 128, row[k] >= 0 ? 16 : 0);
         if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit)) break;
 #pragma unroll
         for (int k = 0; k < NK; ++k)
-          cp_async16(dst + 8 * kChunkBytes + k * (kRows * 128) + swz,
+          cp_async16(land + 8 * kChunkBytes + k * (kRows * 128),
                      p.pe + static_cast<int64_t>(max(row[k], 0)) * (kRope * 2) + piece * 16, row[k] >= 0 ? 16 : 0);
         cp_async_arrive(&ms.full[st][2]);
-      }
+        if (!warp_wait(&ms.empty[st][2], ph ^ 1, abort_flag, &ms.status, limit) ||
+            !warp_wait(&ms.empty[st][3], ph ^ 1, abort_flag, &ms.status, limit))
+          break;
+        cp_async_wait_all();
 #pragma unroll
-      for (int f = 0; f < Sh::kFull; ++f) {
-        if (f > 0 && (flags & kEnd)) break;
+        for (int c = 2; c < 4; ++c)
 #pragma unroll
-        for (int c = Sh::first_part(f); c < Sh::first_part(f + 1); ++c) {
-          if (c > 0 && !(flags & kEnd) &&
-              !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
-          if (FP8) {
-            if (c < 4 && !null) store_part(c, dst);
-          } else if (!null) {
+          for (int k = 0; k < NK; ++k)
+            store_codes(ld_shared16(land + c * kChunkBytes + k * (kRows * 128)), c, k, dst);
+        uint4 raw[2 * NK];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k = 0; k < NK; ++k) raw[NK * c + k] = ld_shared16(land + c * kChunkBytes + k * (kRows * 128));
+        __syncwarp();
+        if (lane == 0 && !withhold) mbar_arrive(&ms.full[st][0]);
+        named_bar_sync(3, kProducers);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k = 0; k < NK; ++k) store_codes(raw[NK * c + k], c, k, dst);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.full[st][1]);
+      } else if (FP8) {
+        // nothing to bring: every thread arrives for the rotated part, a warp for the others
+        for (int f = 0; f < Sh::kFull; ++f) {
+          if (f > 0 && (flags & kEnd)) break;
+          if (f > 0 && !warp_wait(&ms.empty[st][f == 1 ? 1 : 4], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
+          if (f == 2 && (!warp_wait(&ms.empty[st][2], ph ^ 1, abort_flag, &ms.status, limit) ||
+                         !warp_wait(&ms.empty[st][3], ph ^ 1, abort_flag, &ms.status, limit))) { ok = false; break; }
+          __syncwarp();
+          if (f == 2 || lane == 0) mbar_arrive(&ms.full[st][f]);
+        }
+      } else {
+#pragma unroll
+        for (int f = 0; f < Sh::kFull; ++f) {
+          if (f > 0 && (flags & kEnd)) break;
+#pragma unroll
+          for (int c = Sh::first_part(f); c < Sh::end_part(f); ++c) {
+            if (c > 0 && !(flags & kEnd) &&
+                !warp_wait(&ms.empty[st][c], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
+            if (null) continue;
 #pragma unroll
             for (int u = 0; u < (c < 4 ? 2 : 1); ++u)
 #pragma unroll
@@ -667,29 +688,14 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
                 cp_async16(dst + (2 * c + u) * kChunkBytes + k * (kRows * 128) + swz, row_at(row[k]) + (2 * c + u) * 128,
                            row[k] >= 0 ? 16 : 0);
           }
-        }
-        if (!ok) break;
-        if (FP8 && f < 2) {
-          __syncwarp();
-          if (lane == 0 && !(withhold && f == 0)) mbar_arrive(&ms.full[st][f]);
-        } else if (FP8 && !null) {
-          // (its copies went out before part 0)
-        } else if (null) {
-          mbar_arrive(&ms.full[st][f]);
-        } else if (!(withhold && f == 0)) {
-          cp_async_arrive(&ms.full[st][f]);
+          if (!ok) break;
+          if (null) mbar_arrive(&ms.full[st][f]);
+          else if (!(withhold && f == 0)) cp_async_arrive(&ms.full[st][f]);
         }
       }
       if (!ok) break;
       if (flags & kEnd) break;
       advance();
-      // fp8: the next tile's codes, all at once and behind the last use of this
-      // one's: a wait for a register filled by an earlier load would also wait
-      // for loads issued since
-      if (FP8 && !(d.flags & (kNull | kEnd))) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) load_part(c);
-      }
     }
     cp_async_wait_all();
     if (bad) atomicOr(&ms.status, bad);
@@ -735,12 +741,13 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int c = Sh::first_part(f); c < Sh::first_part(f + 1); ++c) {
+          for (int c = Sh::first_part(f); c < Sh::end_part(f); ++c) {
             const uint32_t dd = tbase + (FP8 && c == 4 ? kTmemPe : kTmemS) + st * 64;
 #pragma unroll
             for (int ks = 0; ks < (c < 4 ? 8 : 4); ++ks) {
               const int off = ((2 * c + (ks >> 2)) * kChunkBytes + (ks & 3) * 32) >> 4;
-              mma_16(dd, q_d + off, k_d + off, c == 4 ? id_pe : id_s, ks > 0 || (c > 0 && !(FP8 && c == 4)));
+              mma_16(dd, q_d + off, k_d + off, c == 4 ? id_pe : id_s,
+                     ks > 0 || (c != Sh::first_part(0) && !(FP8 && c == 4)));
             }
           }
           if (f == Sh::kFull - 1) {
@@ -800,6 +807,9 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     // fp8: weights are fp16, whose range the maximum is moved away from the
     // lower end of (2^7 next to it, 2^15 before a rescale; 2^-24 is the smallest)
     constexpr float kBias = FP8 ? 7.f : 0.f;
+    // exchanged between the two warpgroups in the weights' buffer, while no weights are in it
+    float* half_max = reinterpret_cast<float*>(smem + kOffP);
+    float* stat_l1 = half_max;
     uint8_t* prow = smem + kOffP + rr * 128 + 4 * (lane & 3);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float to_log2[2] = {p.scale_log2, p.scale_log2};
@@ -834,7 +844,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 #pragma unroll
           for (int half = 0; half < NJ / 4; ++half) {  // 32 columns at a time
             uint32_t e[16];
-            tmem_ld_16(tbase + kTmemPe + b * 64 + half * 32 + lane_base, e);
+            tmem_ld_16(tbase + kTmemPe + b * 64 + wg * kKeys + half * 32 + lane_base, e);
             tmem_ld_wait();
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
@@ -959,14 +969,14 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           }
           if (kSwg > 1) {
             if ((lane & 3) == 0) {
-              ms.half_max[b][wg][rr] = mx[0];
-              ms.half_max[b][wg][rr + 8] = mx[1];
+              half_max[wg * kAttnCols + rr] = mx[0];
+              half_max[wg * kAttnCols + rr + 8] = mx[1];
             }
             named_bar_sync(2, kSoftmax);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (kSwg > 1) mx[h] = fmaxf(mx[h], ms.half_max[b][wg ^ 1][rr + 8 * h]);
+            if (kSwg > 1) mx[h] = fmaxf(mx[h], half_max[(wg ^ 1) * kAttnCols + rr + 8 * h]);
             float fac = 1.f;
             if (flags & kFirst) {
               m[h] = mx[h];
@@ -1027,24 +1037,24 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 
       // ---- the segment's end: its sums, divided (a whole group) or as they are (a cut one)
       const int group = f.group, slot = f.piece;
+      const bool none = (flags & kNull) && (flags & kFirst);  // no key at all: the sums were never written
+      const bool direct = flags & kDirect;
+      if (!warp_wait(&ms.pv_done, i & 1, abort_flag, &ms.status, limit)) dead = true;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
         l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
         if ((lane & 3) == 0) {
           if (wg == 0) ms.stat_m[rr + 8 * h] = m[h];
-          (wg == 0 ? ms.stat_l : ms.stat_l1)[rr + 8 * h] = l[h];
+          (wg == 0 ? ms.stat_l : stat_l1)[rr + 8 * h] = l[h];
         }
       }
-      const bool none = (flags & kNull) && (flags & kFirst);  // no key at all: the sums were never written
-      const bool direct = flags & kDirect;
-      if (!warp_wait(&ms.pv_done, i & 1, abort_flag, &ms.status, limit)) dead = true;
       if (bar_red_or(1, kSoftmax, dead)) break;
       tc_fence_after();
       const int n = min(kAttnCols, cols - cg * kAttnCols);
       const int64_t col0 = static_cast<int64_t>(group) * cols + cg * kAttnCols;
       if (tid < kAttnCols) {
-        const float mm = ms.stat_m[tid], ll = kSwg > 1 ? ms.stat_l[tid] + ms.stat_l1[tid] : ms.stat_l[tid];
+        const float mm = ms.stat_m[tid], ll = kSwg > 1 ? ms.stat_l[tid] + stat_l1[tid] : ms.stat_l[tid];
         if (tid < n) {
           if (!direct) p.part_ml[static_cast<int64_t>(slot) * kAttnCols + tid] = make_float2(mm, ll);
           else if (p.lse) p.lse[col0 + tid] = (mm + log2f(ll)) * 0.69314718055994531f;
