@@ -200,6 +200,17 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// The same for 4 bytes.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Orders this thread's view of generic-proxy writes before later async-proxy
 // (tensor core) reads of the same shared memory.
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 
     // ---- the tile about to be written
     Info d;
-    float sc = 0.f;
+    int key_slot = -1;       // fp8: pool slot of key pt
     int row[NK];             // pool slots of its rows r0 + kRows k, -1 where there is none
     const int num_slots = static_cast<int>(p.num_slots), num_pages = num_slots / kPageSize;
     // Finds the next tile that holds keys (or ends a segment, or the stream) and describes it in d.
@@ -494,10 +505,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           for (int k = 0; k < NK; ++k) {
             row[k] = __shfl_sync(0xFFFFFFFFu, sl[kRows * k >> 5], (r0 + kRows * k) & 31);
           }
-          if (FP8 && pt < kAttnKeys) {
-            const int v = pt < 32 ? sl[0] : sl[1];
-            sc = v >= 0 ? __ldg(p.s + v) : 1.f;
-          }
+          if (FP8 && pt < kAttnKeys) key_slot = pt < 32 ? sl[0] : sl[1];
         }
         return;
       }
@@ -608,13 +616,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         ms.info[i & (kInfo - 1)] = d;
         if (!FP8) mbar_arrive(&ms.full[st][0]);
       }
-      if (FP8 && pt < kAttnKeys) {
-        // a scale of 0 (or below 2^-60) counts as 2^-60: its log and inverse are used
-        const float x = sc < 8.673617379884035e-19f ? 8.673617379884035e-19f : sc;
-        ms.scale[st][0][pt] = x;
-        ms.scale[st][1][pt] = log2f(x);
-        ms.scale[st][2][pt] = 1.f / x;
-      }
       if (FP8 && (flags & kFirst) && !null && piece == 0) {
 #pragma unroll
         for (int k = 0; k < NK; ++k) ms.q_scale[st][r0 + kRows * k] = qfac[k];
@@ -628,33 +629,55 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         // into registers, and when all have, they become fp16 in the first.
         if (!warp_wait(&ms.empty[st][1], ph ^ 1, abort_flag, &ms.status, limit)) break;
         const uint32_t land = dst + swz;
+        if (pt < kAttnKeys) cp_async4(smem_u32(&ms.scale[st][0][pt]), p.s + max(key_slot, 0), key_slot >= 0 ? 4 : 0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int k = 0; k < NK; ++k) {
+          const uint8_t* at = row_at(row[k]);
+          const uint32_t n = row[k] >= 0 ? 16 : 0;
+          cp_async16(land + 2 * kChunkBytes + k * (kRows * 128), at + 2 * 128, n);
+          cp_async16(land + 3 * kChunkBytes + k * (kRows * 128), at + 3 * 128, n);
+        }
+        cp_async_commit();
 #pragma unroll
-          for (int k = 0; k < NK; ++k)
-            cp_async16(land + c * kChunkBytes + k * (kRows * 128), row_at(row[k]) + c * 128, row[k] >= 0 ? 16 : 0);
+        for (int k = 0; k < NK; ++k) {
+          const uint8_t* at = row_at(row[k]);
+          const uint32_t n = row[k] >= 0 ? 16 : 0;
+          cp_async16(land + k * (kRows * 128), at, n);
+          cp_async16(land + kChunkBytes + k * (kRows * 128), at + 128, n);
+        }
+        cp_async_commit();
         if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit)) break;
 #pragma unroll
         for (int k = 0; k < NK; ++k)
           cp_async16(land + 8 * kChunkBytes + k * (kRows * 128),
                      p.pe + static_cast<int64_t>(max(row[k], 0)) * (kRope * 2) + piece * 16, row[k] >= 0 ? 16 : 0);
         cp_async_arrive(&ms.full[st][2]);
+        cp_async_commit();
         if (!warp_wait(&ms.empty[st][2], ph ^ 1, abort_flag, &ms.status, limit) ||
             !warp_wait(&ms.empty[st][3], ph ^ 1, abort_flag, &ms.status, limit))
           break;
-        cp_async_wait_all();
+        cp_async_wait<2>();
+        if (pt < kAttnKeys) {
+          // a scale of 0 (or below 2^-60, or of a key that does not exist)
+          // counts as 2^-60: its log and inverse are used
+          const float x = ms.scale[st][0][pt], y = x < 8.673617379884035e-19f ? 8.673617379884035e-19f : x;
+          ms.scale[st][0][pt] = y;
+          ms.scale[st][1][pt] = log2f(y);
+          ms.scale[st][2][pt] = 1.f / y;
+        }
 #pragma unroll
         for (int c = 2; c < 4; ++c)
 #pragma unroll
           for (int k = 0; k < NK; ++k)
             store_codes(ld_shared16(land + c * kChunkBytes + k * (kRows * 128)), c, k, dst);
+        __syncwarp();
+        if (lane == 0 && !withhold) mbar_arrive(&ms.full[st][0]);
+        cp_async_wait<1>();
         uint4 raw[2 * NK];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int k = 0; k < NK; ++k) raw[NK * c + k] = ld_shared16(land + c * kChunkBytes + k * (kRows * 128));
-        __syncwarp();
-        if (lane == 0 && !withhold) mbar_arrive(&ms.full[st][0]);
         named_bar_sync(3, kProducers);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
