@@ -80,9 +80,13 @@ int check_strides(const char* what, const void* ptr, int64_t a, int64_t b) {
   return FP8IDX_OK;
 }
 
+int check_scale(float scale) {
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(FP8IDX_EINVAL, "scale must be positive and finite");
+  return FP8IDX_OK;
+}
+
 int run_attn(LatentAttnParams& p, const AttnPlan& pl, bool paged, bool fp8, void* ws, size_t ws_bytes, float scale,
              void* stream) {
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(FP8IDX_EINVAL, "scale must be positive and finite");
   if (!ws || !aligned(ws, 256)) return fail(FP8IDX_EINVAL, "workspace must be non-null and 256-byte aligned");
   if (ws_bytes < pl.total)
     return fail(FP8IDX_EWORKSPACE, "workspace too small (%zu < %zu bytes)", ws_bytes, pl.total);
@@ -173,6 +177,7 @@ int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int6
                                    int H, int latent, int rope, float scale, uint16_t* out, float* lse, void* ws,
                                    size_t ws_bytes, void* stream) {
   FP8IDX_TRY(check_latent_shape(H, latent, rope));
+  FP8IDX_TRY(check_scale(scale));
   if (rows < 0 || topk < 0) return fail(FP8IDX_EINVAL, "negative size");
   if (rows > (int64_t(1) << 25) || topk > (1 << 24) || rows * (topk_tiles(topk) + 1) >= (int64_t(1) << 31))
     return fail(FP8IDX_EINVAL, "size too large");
@@ -218,6 +223,7 @@ int fp8idx_paged_latent_attention(const uint16_t* q, int64_t q_row_stride, int64
                                   int max_blocks, int64_t num_pages, int page_size, int H, int latent, int rope,
                                   float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   FP8IDX_TRY(check_latent_shape(H, latent, rope));
+  FP8IDX_TRY(check_scale(scale));
   if (page_size != kPageSize) return fail(FP8IDX_EUNSUPPORTED, "page_size must be 64 (got %d)", page_size);
   if (R < 1 || R > 8) return fail(FP8IDX_EUNSUPPORTED, "rows per request must be in [1, 8] (got %d)", R);
   if (B < 0 || num_pages < 0 || max_blocks < 1) return fail(FP8IDX_EINVAL, "bad sizes");
