@@ -387,8 +387,12 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
   __syncthreads();
   tc_fence_after();
   const int64_t parts = min(static_cast<int64_t>(p.parts), total);
-  const int64_t x0 = part < parts ? part * total / parts : 0;
-  const int64_t x1 = part < parts ? (part + 1) * total / parts : 0;
+  int64_t x0 = part < parts ? part * total / parts : 0;
+  int64_t x1 = part < parts ? (part + 1) * total / parts : 0;
+  if (!PAGED && p.whole_groups) {  // ranges that end with groups
+    x0 = static_cast<int64_t>(part) * p.groups / p.parts * tiles_of(p.topk);
+    x1 = static_cast<int64_t>(part + 1) * p.groups / p.parts * tiles_of(p.topk);
+  }
   const uint32_t tbase = ms.tmem;
   if (too_long) atomicOr(&ms.status, kStatusSeqLenTooLong);
 
@@ -436,6 +440,8 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         ms.cut = make_int2(g, c1 - part + 1);
       }
       from_start = t == 0;
+      if (t == 0 && pt == 0 && p.groups <= kSpreadGroups)
+        p.group_meta[g * p.ncg + cg] = make_int2(static_cast<int>(blockIdx.x), te < nt ? ms.cut.y : 1);
       list = PAGED ? p.block_table + static_cast<int64_t>(g) * p.max_blocks
                    : p.slots + static_cast<int64_t>(g) * p.ld_slots;
       left -= te - t;
@@ -547,6 +553,10 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       cp_async_wait_all();
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
+        if (cg * kAttnCols + kRows * k >= p.R * p.H) {  // no such columns (zeros)
+          fac[k] = 0.f;
+          continue;
+        }
         uint8_t* at = smem + kOffQ + (r0 + kRows * k) * 128 + swz;
         uint32_t top = 0;
 #pragma unroll
@@ -562,19 +572,18 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
         const int ex = top >> 7;  // biased exponent of the largest value
-        // times 2^(140 - ex), as two factors that are ordinary numbers; a zero or non-finite column stays
-        const int up = ex == 0 || ex == 255 ? 0 : 140 - ex, up0 = up / 2, up1 = up - up0;
-        const float f0 = __uint_as_float(static_cast<uint32_t>(127 + up0) << 23);
-        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up1) << 23);
-        fac[k] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up0) << 23) *
-                 __uint_as_float(static_cast<uint32_t>(127 - up1) << 23);
+        // times 2^(140 - ex), at most 2^126 so that its inverse is an ordinary
+        // number too; a zero or non-finite column stays
+        const int up = ex == 0 || ex == 255 ? 0 : min(140 - ex, 126);
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        fac[k] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           uint4 v = *reinterpret_cast<const uint4*>(at + c * kChunkBytes);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t y = (&v.x)[e];
-            const float lo = __uint_as_float(y << 16) * f0 * f1, hi = __uint_as_float(y & 0xFFFF0000u) * f0 * f1;
+            const float lo = __uint_as_float(y << 16) * f, hi = __uint_as_float(y & 0xFFFF0000u) * f;
             (&v.x)[e] = c < 8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
           }
           *reinterpret_cast<uint4*>(at + c * kChunkBytes) = v;
@@ -1181,65 +1190,154 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 }
 
 // ---------------------------------------------------------------- joining cut groups
+//
+// A cut group's pieces lie in the CTAs x, x + ncg, ..., in key order: the first
+// in its second slot, the others in their first.  With (m_k, l_k, O_k) the
+// pieces' reference maxima, sums and unnormalised results,
+//   w_k = 2^(m_k - max m) / sum_k l_k 2^(m_k - max m),   out = sum_k w_k O_k.
+// Bound by latency: the pieces come from L2 (at most two a CTA, 128 KB each
+// with 64 columns).
 
-// Block (x, y): the group whose first piece CTA x holds, value block y % 4,
-// columns [4 QPB (y / 4), + 4 QPB).  The pieces lie in the CTAs x, x + ncg,
-// ..., in key order: the first in its second slot, the others in their first.
-// Four sets of 128 threads, one value each.  With few pieces a set takes a
-// column quad of its own; with many (a long group over all SMs) it takes every
-// fourth piece, and the sets' sums are joined.  A thread's first loads go out
-// before the weights are known.  QPB is 4, or 1 where few groups can be cut:
-// more blocks then share a group's pieces.
-constexpr int kJoinThreads = 512, kJoinAhead = 8;
-constexpr int kSpreadGroups = 8;  // "few groups"
+__device__ __forceinline__ int64_t piece_slot(int x, int k, int ncg) {
+  return static_cast<int64_t>(x + k * ncg) * 2 + (k == 0 ? 1 : 0);
+}
 
-template <int QPB>
+// The call's status block: every CTA's bits.
+__device__ __forceinline__ void collect_status(const LatentAttnParams& p) {
+  int bits = 0;
+  for (int k = threadIdx.x; k < p.parts * p.ncg; k += blockDim.x) bits |= p.meta[k].z;
+  bits = (__syncthreads_or(bits & kStatusWaitTimeout) ? kStatusWaitTimeout : 0) |
+         (__syncthreads_or(bits & kStatusBadPage) ? kStatusBadPage : 0) |
+         (__syncthreads_or(bits & kStatusSeqLenTooLong) ? kStatusSeqLenTooLong : 0) |
+         (__syncthreads_or(bits & kStatusBadSlot) ? kStatusBadSlot : 0);
+  if (threadIdx.x < kStatusBytes / 4) p.status[threadIdx.x] = threadIdx.x == 0 ? bits : 0;
+}
+
+__device__ __forceinline__ float4 piece_at(const LatentAttnParams& p, int64_t slot, int vb, int quad, int val) {
+  return *reinterpret_cast<const float4*>(p.part_o + slot * (kAttnCols * kLatent) +
+                                          ((vb * 2 + (quad >> 3)) * 8 + (quad & 7)) * 512 + val * 4);
+}
+__device__ __forceinline__ void fma4(float4& acc, const float4& v, const float4& w) {
+  acc.x = fmaf(v.x, w.x, acc.x);
+  acc.y = fmaf(v.y, w.y, acc.y);
+  acc.z = fmaf(v.z, w.z, acc.z);
+  acc.w = fmaf(v.w, w.w, acc.w);
+}
+__device__ __forceinline__ void write4(const LatentAttnParams& p, const float4& acc, int64_t oc, int n, int quad, int vb,
+                                       int val) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (4 * quad + e < n)
+      p.out[(oc + 4 * quad + e) * kLatent + vb * 128 + val] = static_cast<uint16_t>(pack_bf16((&acc.x)[e], 0.f));
+}
+
+// The usual form: a group has been cut in two or three, and there are up to a
+// group per CTA.  Block (x, y): the group whose first piece CTA x holds, value
+// block y, all columns: two sets of 128 threads (one value each) take every
+// second column quad, all their loads of a piece under way at once.
+constexpr int kJoinThreads = 256, kJoinChunk = 32;
+
 __global__ void __launch_bounds__(kJoinThreads) latent_combine_kernel(const __grid_constant__ LatentAttnParams p) {
-  __shared__ float4 wt[kAttnMaxParts][QPB];
+  __shared__ float4 wt[kJoinChunk][kAttnCols / 4];
+  __shared__ float2 top_inv[kAttnCols];
+  griddep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0) collect_status(p);
+  const int4 mt = p.meta[blockIdx.x];
+  const int np = mt.y, x = blockIdx.x, vb = blockIdx.y;
+  if (np < 2) return;
+  const int cols = p.R * p.H, cg = x % p.ncg;
+  const int n = min(kAttnCols, cols - cg * kAttnCols), quads = (n + 3) / 4;
+  const int64_t oc = static_cast<int64_t>(mt.x) * cols + cg * kAttnCols;
+  const int sub = tid >> 7, val = tid & 127;
+  float4 acc[8], ahead[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (sub + 2 * u < quads) ahead[u] = piece_at(p, piece_slot(x, 0, p.ncg), vb, sub + 2 * u, val);
+  }
+  for (int c = warp; c < n; c += kJoinThreads / 32) {
+    // one warp a column: the largest reference and the sum over all pieces
+    float top = -INFINITY, sum = 0.f;
+    for (int k = lane; k < np; k += 32) top = fmaxf(top, p.part_ml[piece_slot(x, k, p.ncg) * kAttnCols + c].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int k = lane; k < np; k += 32) {
+      const float2 ml = p.part_ml[piece_slot(x, k, p.ncg) * kAttnCols + c];
+      sum = fmaf(ml.y, exp2f(ml.x - ref), sum);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (lane == 0) {
+      top_inv[c] = make_float2(ref, sum == 0.f ? 0.f : 1.f / sum);
+      if (vb == 0 && p.lse) p.lse[oc + c] = (top + log2f(sum)) * 0.69314718055994531f;
+    }
+  }
+  for (int k0 = 0; k0 < np; k0 += kJoinChunk) {
+    const int nk = min(kJoinChunk, np - k0);
+    __syncthreads();
+    for (int e = tid; e < nk * kAttnCols; e += kJoinThreads) {
+      const int k = e / kAttnCols, c = e % kAttnCols;
+      if (c < n) {
+        const float2 ti = top_inv[c];
+        (&wt[k][c >> 2].x)[c & 3] = exp2f(p.part_ml[piece_slot(x, k0 + k, p.ncg) * kAttnCols + c].x - ti.x) * ti.y;
+      }
+    }
+    __syncthreads();
+    for (int k = 0; k < nk; ++k) {
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = ahead[u];
+      if (k0 + k + 1 < np) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (sub + 2 * u < quads) ahead[u] = piece_at(p, piece_slot(x, k0 + k + 1, p.ncg), vb, sub + 2 * u, val);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (sub + 2 * u < quads) fma4(acc[u], v[u], wt[k][sub + 2 * u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    if (sub + 2 * u < quads) write4(p, acc[u], oc, n, sub + 2 * u, vb, val);
+}
+
+// The form for few groups (at most kSpreadGroups, so each may be cut into many
+// pieces).  Block (x, y): group x / ncg, column block x % ncg, value block
+// y % 4, column quad y / 4.  Four sets of 128 threads take every fourth piece,
+// and their sums are joined; the first loads go out before the weights are known.
+constexpr int kSpreadThreads = 512, kSpreadAhead = 8;
+
+__global__ void __launch_bounds__(kSpreadThreads) latent_spread_kernel(const __grid_constant__ LatentAttnParams p) {
+  __shared__ float4 wt[kAttnMaxParts];
   __shared__ float4 acc_of[3][128];
   griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    // the call's status block: every CTA's bits
-    int bits = 0;
-    for (int k = tid; k < static_cast<int>(gridDim.x); k += kJoinThreads) bits |= p.meta[k].z;
-    bits = (__syncthreads_or(bits & kStatusWaitTimeout) ? kStatusWaitTimeout : 0) |
-           (__syncthreads_or(bits & kStatusBadPage) ? kStatusBadPage : 0) |
-           (__syncthreads_or(bits & kStatusSeqLenTooLong) ? kStatusSeqLenTooLong : 0) |
-           (__syncthreads_or(bits & kStatusBadSlot) ? kStatusBadSlot : 0);
-    if (tid < kStatusBytes / 4) p.status[tid] = tid == 0 ? bits : 0;
-  }
-  const int4 mt = p.meta[blockIdx.x];
-  const int np = mt.y;
+  if (blockIdx.x == 0 && blockIdx.y == 0) collect_status(p);
+  const int2 e = p.group_meta[blockIdx.x];
+  const int x = e.x, np = e.y;
   if (np < 2) return;
   const int cols = p.R * p.H, cg = blockIdx.x % p.ncg;
   const int n = min(kAttnCols, cols - cg * kAttnCols);
-  const int q0 = (blockIdx.y >> 2) * QPB, vb = blockIdx.y & 3;
-  const int nq = min(QPB, (n + 3) / 4 - q0);  // column quads of this block
-  if (nq <= 0) return;
-  const int64_t oc = static_cast<int64_t>(mt.x) * cols + cg * kAttnCols;
-  auto slot_at = [&](int k) { return static_cast<int64_t>(blockIdx.x + k * p.ncg) * 2 + (k == 0 ? 1 : 0); };
+  const int quad = blockIdx.y >> 2, vb = blockIdx.y & 3;
+  if (4 * quad >= n) return;
+  const int64_t oc = static_cast<int64_t>(blockIdx.x / p.ncg) * cols + cg * kAttnCols;
   const int sub = tid >> 7, val = tid & 127;
-  auto at = [&](int quad, int k) {
-    return *reinterpret_cast<const float4*>(p.part_o + slot_at(k) * (kAttnCols * kLatent) +
-                                            ((vb * 2 + (quad >> 3)) * 8 + (quad & 7)) * 512 + val * 4);
-  };
-  const bool few = QPB == 4 && np <= kJoinAhead;
-  float4 first[kJoinAhead];
+  float4 first[kSpreadAhead];
 #pragma unroll
-  for (int u = 0; u < kJoinAhead; ++u) {
-    const int k = few ? u : sub + 4 * u;
-    first[u] = k < np && (!few || sub < nq) ? at(few ? q0 + sub : q0, k) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  for (int c = warp; c < 4 * nq; c += kJoinThreads / 32) {
-    // one warp: the weights of column 4 q0 + c in every piece
-    const int col = 4 * q0 + c;
+  for (int u = 0; u < kSpreadAhead; ++u)
+    if (sub + 4 * u < np) first[u] = piece_at(p, piece_slot(x, sub + 4 * u, p.ncg), vb, quad, val);
+  if (warp < 4) {
+    // warp w: the weights of column 4 quad + w in every piece
+    const int col = 4 * quad + warp;
     float2 ml[kAttnMaxParts / 32];
     float top = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kAttnMaxParts / 32; ++u) {
       const int k = lane + 32 * u;
-      ml[u] = col < n && k < np ? p.part_ml[slot_at(k) * kAttnCols + col] : make_float2(-INFINITY, 0.f);
+      ml[u] = col < n && k < np ? p.part_ml[piece_slot(x, k, p.ncg) * kAttnCols + col] : make_float2(-INFINITY, 0.f);
       top = fmaxf(top, ml[u].x);
     }
 #pragma unroll
@@ -1256,59 +1354,28 @@ __global__ void __launch_bounds__(kJoinThreads) latent_combine_kernel(const __gr
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int u = 0; u < kAttnMaxParts / 32; ++u)
-      if (lane + 32 * u < np) (&wt[lane + 32 * u][c >> 2].x)[c & 3] = ml[u].x * inv;
+      if (lane + 32 * u < np) (&wt[lane + 32 * u].x)[warp] = ml[u].x * inv;
     if (vb == 0 && lane == 0 && p.lse && col < n) p.lse[oc + col] = (top + log2f(sum)) * 0.69314718055994531f;
   }
   __syncthreads();
-  float4 acc;
-  auto add = [&](const float4& v, const float4& w) {
-    acc.x = fmaf(v.x, w.x, acc.x);
-    acc.y = fmaf(v.y, w.y, acc.y);
-    acc.z = fmaf(v.z, w.z, acc.z);
-    acc.w = fmaf(v.w, w.w, acc.w);
-  };
-  auto write = [&](int quad) {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (4 * quad + e < n)
-        p.out[(oc + 4 * quad + e) * kLatent + vb * 128 + val] = static_cast<uint16_t>(pack_bf16((&acc.x)[e], 0.f));
-  };
-  if (few) {
-    if (sub >= nq) return;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < kJoinAhead; ++u)
-      if (u < np) add(first[u], wt[u][sub]);
-    write(q0 + sub);
-    return;
-  }
-  for (int q = 0; q < nq; ++q) {
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (q > 0) {
-#pragma unroll
-      for (int u = 0; u < kJoinAhead; ++u)
-        first[u] = sub + 4 * u < np ? at(q0 + q, sub + 4 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int u = 0; u < kJoinAhead; ++u)
-      if (sub + 4 * u < np) add(first[u], wt[sub + 4 * u][q]);
+  for (int u = 0; u < kSpreadAhead; ++u)
+    if (sub + 4 * u < np) fma4(acc, first[u], wt[sub + 4 * u]);
 #pragma unroll 4
-    for (int k = sub + 4 * kJoinAhead; k < np; k += 4) add(at(q0 + q, k), wt[k][q]);
-    if (sub > 0) acc_of[sub - 1][val] = acc;
-    __syncthreads();
-    if (sub == 0) {
+  for (int k = sub + 4 * kSpreadAhead; k < np; k += 4) fma4(acc, piece_at(p, piece_slot(x, k, p.ncg), vb, quad, val), wt[k]);
+  if (sub > 0) acc_of[sub - 1][val] = acc;
+  __syncthreads();
+  if (sub > 0) return;
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const float4 v = acc_of[u][val];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      write(q0 + q);
-    }
-    __syncthreads();
+  for (int u = 0; u < 3; ++u) {
+    const float4 v = acc_of[u][val];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
   }
+  write4(p, acc, oc, n, quad, vb, val);
 }
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, cudaStream_t st) {
@@ -1336,16 +1403,16 @@ cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, bool paged, 
   void* args[] = {&copy};
   e = cudaLaunchKernelExC(&cfg, kern, args);
   if (e != cudaSuccess) return e;
-  // four value blocks x column quads (all a block can hold, or one where few groups can be cut)
-  const int quads = (min(kAttnCols, p.R * p.H) + 3) / 4;
-  const bool spread = p.groups <= kSpreadGroups;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(4 * (spread ? quads : (quads + 3) / 4)));
-  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelExC(&cfg,
-                             spread ? reinterpret_cast<const void*>(latent_combine_kernel<1>)
-                                    : reinterpret_cast<const void*>(latent_combine_kernel<4>),
-                             args);
+  if (p.groups <= kSpreadGroups) {
+    cfg.gridDim = dim3(static_cast<unsigned>(p.groups * p.ncg), static_cast<unsigned>(4 * ((min(kAttnCols, p.R * p.H) + 3) / 4)));
+    cfg.blockDim = dim3(kSpreadThreads);
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(latent_spread_kernel), args);
+  }
+  // (no group is cut where the ranges end with groups: the status alone)
+  cfg.gridDim = p.whole_groups ? dim3(1) : dim3(static_cast<unsigned>(grid), 4);
+  cfg.blockDim = dim3(kJoinThreads);
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(latent_combine_kernel), args);
 }
 
 }  // namespace fp8idx

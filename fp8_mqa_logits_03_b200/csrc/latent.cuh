@@ -15,6 +15,7 @@ constexpr int kAttnKeys = 64;                // keys per tile (one page)
 constexpr int kAttnCols = 64;                // (row, head) columns of a unit
 constexpr int kAttnMaxHeads = 128;
 constexpr int kAttnMaxParts = 256;            // ranges of the tile axis
+constexpr int kSpreadGroups = 8;              // groups that are joined by latent_spread_kernel
 constexpr int kStatusBadSlot = 16;           // device status bit: a selected slot past the pool
 
 struct LatentStoreParams {
@@ -60,10 +61,12 @@ struct LatentAttnParams {
   // schedule: the groups' tiles back to back, cut into `parts` equal ranges;
   // CTA x takes column block x % ncg of range x / ncg
   int ncg, parts;
+  int whole_groups;         // selected form: ranges end with groups, none is cut
   int* status;
   float* part_o;            // [grid][2][64 x 512] unnormalised sums of cut groups
   float2* part_ml;          // [grid][2][64] (reference maximum in log2 units, sum)
   int4* meta;               // [grid] (group, pieces) of the cut group whose first piece the CTA holds, status bits
+  int2* group_meta;         // [groups x ncg] (first CTA, pieces), where groups <= kSpreadGroups
   unsigned long long wait_limit_ns;
   int debug_withhold_first_tile;
 };

@@ -31,26 +31,42 @@ int sms_cached() {
 
 struct AttnPlan {
   int ncg = 1, parts = 1;
-  size_t off_meta = 0, off_ml = 0, off_o = 0, total = 0;
+  bool whole_groups = false;
+  size_t off_meta = 0, off_group = 0, off_ml = 0, off_o = 0, total = 0;
 };
+
+// What joining cut groups costs, in tiles of a CTA's time.
+constexpr int64_t kJoinTiles = 4;
 
 // One CTA per SM, split into column blocks of 64 (a block of every range runs
 // at the same time as the others of that range, so that they share its keys
 // in L2) and as many ranges of the tile axis as fit; a range holds at least
-// one tile.
-AttnPlan plan_attn(int64_t groups, int64_t cols, int64_t max_tiles_per_group, int sms) {
+// one tile.  Where all groups have the same number of tiles (`uniform`), the
+// ranges end with groups if that makes the longest one at most kJoinTiles
+// longer: nothing is then left to be joined.
+AttnPlan plan_attn(int64_t groups, int64_t cols, int64_t tiles_per_group, bool uniform, int sms) {
   AttnPlan pl;
   pl.ncg = static_cast<int>(ceil_div(cols, kAttnCols));
-  const int64_t tiles = std::max<int64_t>(1, groups * std::max<int64_t>(1, max_tiles_per_group));
+  const int64_t nt = std::max<int64_t>(1, tiles_per_group);
+  const int64_t tiles = std::max<int64_t>(1, groups * nt);
   pl.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / pl.ncg, tiles, kAttnMaxParts})));
+  if (uniform && groups > 0) {
+    const int64_t most = std::min<int64_t>(pl.parts, groups), each = ceil_div(groups, most);
+    if (each * nt <= ceil_div(tiles, pl.parts) + kJoinTiles) {
+      pl.whole_groups = true;
+      pl.parts = static_cast<int>(ceil_div(groups, each));
+    }
+  }
   const int64_t grid = static_cast<int64_t>(pl.parts) * pl.ncg;
   int64_t off = kStatusBytes;
   pl.off_meta = off;
   off += round_up(grid * 16, 256);
+  pl.off_group = off;
+  off += round_up(kSpreadGroups * static_cast<int64_t>(pl.ncg) * 8, 256);
   pl.off_ml = off;
   off += round_up(grid * 2 * kAttnCols * 8, 256);
   pl.off_o = off;
-  off += grid * 2 * kAttnCols * kLatent * 4;
+  if (!pl.whole_groups) off += grid * 2 * kAttnCols * kLatent * 4;
   pl.total = static_cast<size_t>(off);
   return pl;
 }
@@ -94,6 +110,8 @@ int run_attn(LatentAttnParams& p, const AttnPlan& pl, bool paged, bool fp8, void
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.ncg = pl.ncg;
   p.parts = pl.parts;
+  p.whole_groups = pl.whole_groups ? 1 : 0;
+  p.group_meta = reinterpret_cast<int2*>(wsb + pl.off_group);
   p.status = reinterpret_cast<int*>(wsb);
   p.meta = reinterpret_cast<int4*>(wsb + pl.off_meta);
   p.part_ml = reinterpret_cast<float2*>(wsb + pl.off_ml);
@@ -168,7 +186,7 @@ size_t fp8idx_sparse_latent_attention_workspace(int64_t rows, int H, int topk) {
   if (rows < 0 || H < 1 || H > kAttnMaxHeads || topk < 0) return 0;
   const int sms = sms_cached();
   if (sms <= 0) return 0;
-  return plan_attn(rows, H, topk_tiles(topk), sms).total;
+  return plan_attn(rows, H, topk_tiles(topk), true, sms).total;
 }
 
 int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -207,14 +225,14 @@ int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int6
   p.H = H;
   p.out = out;
   p.lse = lse;
-  return run_attn(p, plan_attn(rows, H, topk_tiles(topk), sms), false, s_pool != nullptr, ws, ws_bytes, scale, stream);
+  return run_attn(p, plan_attn(rows, H, topk_tiles(topk), true, sms), false, s_pool != nullptr, ws, ws_bytes, scale, stream);
 }
 
 size_t fp8idx_paged_latent_attention_workspace(int64_t B, int R, int max_blocks, int H) {
   if (B < 0 || R < 1 || R > 8 || H < 1 || H > kAttnMaxHeads || max_blocks < 1) return 0;
   const int sms = sms_cached();
   if (sms <= 0) return 0;
-  return plan_attn(B, static_cast<int64_t>(R) * H, max_blocks, sms).total;
+  return plan_attn(B, static_cast<int64_t>(R) * H, max_blocks, false, sms).total;
 }
 
 int fp8idx_paged_latent_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -256,7 +274,7 @@ int fp8idx_paged_latent_attention(const uint16_t* q, int64_t q_row_stride, int64
   p.H = H;
   p.out = out;
   p.lse = lse;
-  return run_attn(p, plan_attn(B, static_cast<int64_t>(R) * H, max_blocks, sms), true, s_pages != nullptr, ws, ws_bytes,
+  return run_attn(p, plan_attn(B, static_cast<int64_t>(R) * H, max_blocks, false, sms), true, s_pages != nullptr, ws, ws_bytes,
                   scale, stream);
 }
 
