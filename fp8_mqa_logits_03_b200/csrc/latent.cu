@@ -143,7 +143,7 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
-// 16 lanes x 64 (or 32) columns: thread t receives, for each 8-column block j, columns
+// 16 lanes x 64 (or 32, 16) columns: thread t receives, for each 8-column block j, columns
 // 8j + 2(t % 4) + {0, 1} of lane t / 4 in r[4j], r[4j+1] and of lane t / 4 + 8
 // in r[4j+2], r[4j+3].
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[32]) {
@@ -158,6 +158,13 @@ __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -238,6 +245,12 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& h
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The larger of each pair of 16-bit halves.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 // Four 8 x 8 matrices of 16-bit values, each stored transposed: this lane
@@ -552,22 +565,20 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     auto convert_q = [&](float (&fac)[NK]) {
       cp_async_wait_all();
 #pragma unroll
+      for (int k = 0; k < NK; ++k) fac[k] = 0.f;
+#pragma unroll 1
       for (int k = 0; k < NK; ++k) {
-        if (cg * kAttnCols + kRows * k >= p.R * p.H) {  // no such columns (zeros)
-          fac[k] = 0.f;
-          continue;
-        }
-        uint8_t* at = smem + kOffQ + (r0 + kRows * k) * 128 + swz;
-        uint32_t top = 0;
+        if (cg * kAttnCols + kRows * k >= p.R * p.H) break;  // no such columns (zeros)
+        const uint32_t at = smem_u32(smem + kOffQ) + (r0 + kRows * k) * 128 + swz;
+        uint4 v[kChunks];
+        uint32_t top = 0;  // largest magnitudes of the two halves of a word
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          const uint4 v = *reinterpret_cast<const uint4*>(at + c * kChunkBytes);
+          v[c] = ld_shared16(at + c * kChunkBytes);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t y = (&v.x)[e] & 0x7FFF7FFFu;
-            top = max(top, max(y & 0xFFFFu, y >> 16));
-          }
+          for (int e = 0; e < 4; ++e) top = max_u16x2(top, (&v[c].x)[e] & 0x7FFF7FFFu);
         }
+        top = max(top & 0xFFFFu, top >> 16);
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
@@ -576,17 +587,19 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         // number too; a zero or non-finite column stays
         const int up = ex == 0 || ex == 255 ? 0 : min(140 - ex, 126);
         const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-        fac[k] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+        for (int u = 0; u < NK; ++u)
+          if (u == k) fac[u] = back;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          uint4 v = *reinterpret_cast<const uint4*>(at + c * kChunkBytes);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t y = (&v.x)[e];
+            const uint32_t y = (&v[c].x)[e];
             const float lo = __uint_as_float(y << 16) * f, hi = __uint_as_float(y & 0xFFFF0000u) * f;
-            (&v.x)[e] = c < 8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+            (&v[c].x)[e] = c < 8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
           }
-          *reinterpret_cast<uint4*>(at + c * kChunkBytes) = v;
+          st_shared16(at + c * kChunkBytes, v[c].x, v[c].y, v[c].z, v[c].w);
         }
       }
       mbar_arrive(&ms.q_full);
@@ -1095,79 +1108,92 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
       named_bar_sync(2, kSoftmax);
       if (direct) {
-        // 16 values x this warpgroup's columns at a time: divided, rounded,
-        // transposed through the warp's part of the weights' buffer, and
-        // written as 16-byte pieces (8 values of one column)
-        // (32 columns: twice as many would spill)
-        constexpr int NC = 32;
-#pragma unroll 1
-        for (int cb = wg * NC; cb < n; cb += kSwg * NC) {
-          float inv[NC / 4];
-#pragma unroll
-          for (int j = 0; j < NC / 8; ++j) {
-            const float2 v = *reinterpret_cast<const float2*>(&ms.stat_l[cb + 8 * j + 2 * (lane & 3)]);
-            inv[2 * j] = v.x;
-            inv[2 * j + 1] = v.y;
-          }
-          uint8_t* tb = smem + kOffP + warp * (NC * 32);
-          const int mrow = (lane >> 4) * 8 + (lane & 7);  // stmatrix: this lane's column (of 16) and value half
-          const uint32_t maddr = smem_u32(tb) + mrow * 32 + ((((lane >> 3) & 1) ^ ((mrow >> 2) & 1)) << 4);
-          uint16_t* oo = p.out + (col0 + cb) * kLatent + quad * 32;
-          uint32_t o[NC / 2], ahead[NC / 2];
+        // This warpgroup's 32 columns: 32 values x 16 columns at a time,
+        // divided, rounded, transposed through the warp's part of the weights'
+        // buffer, and written as 64 bytes a column by four lanes.
+        const int cb = wg * 32;
+        uint8_t* tb = smem + kOffP + warp * 1024;  // [16 columns][32 values], pieces swizzled
+        const int mcol = (lane & 7) + (lane >> 4) * 8, mhalf = (lane >> 3) & 1;  // stmatrix: this lane's column, value half
+        uint16_t* oo = p.out + (col0 + cb) * kLatent + quad * 32;
+        if (cb < n) {
+          uint32_t o[16], ahead[16];
+          // block c: values 128 (c / 2) + 32 quad + {0 .. 31}, columns cb + 16 (c % 2) + {0 .. 15}
           auto fetch = [&](int c) {
-            tmem_ld_16(tbase + kTmemO + (c >> 1) * 64 + cb + lane_base + (static_cast<uint32_t>(c & 1) << 20), ahead);
+            uint32_t (&lo)[8] = *reinterpret_cast<uint32_t(*)[8]>(&ahead[0]);
+            uint32_t (&hi)[8] = *reinterpret_cast<uint32_t(*)[8]>(&ahead[8]);
+            const uint32_t at = tbase + kTmemO + (c >> 1) * 64 + cb + (c & 1) * 16 + lane_base;
+            tmem_ld_16(at, lo);
+            tmem_ld_16(at + (16u << 16), hi);
           };
           if (none) {
 #pragma unroll
-            for (int k = 0; k < NC / 2; ++k) ahead[k] = 0;
+            for (int k = 0; k < 16; ++k) ahead[k] = 0;
           } else {
             fetch(0);
           }
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {  // values 128 (c / 2) + 32 quad + 16 (c % 2) + {0 .. 15}
+          for (int c = 0; c < 8; ++c) {
+            if (cb + (c & 1) * 16 >= n) continue;
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < NC / 2; ++k) o[k] = ahead[k];
-            if (!none && c < 7) fetch(c + 1);
+            for (int k = 0; k < 16; ++k) o[k] = ahead[k];
+            if (!none) {
+              const int next = c + 1 < 8 && cb + ((c + 1) & 1) * 16 >= n ? c + 2 : c + 1;
+              if (next < 8) fetch(next);
+            }
+            const float2 i0 = *reinterpret_cast<const float2*>(&ms.stat_l[cb + (c & 1) * 16 + 2 * (lane & 3)]);
+            const float2 i1 = *reinterpret_cast<const float2*>(&ms.stat_l[cb + (c & 1) * 16 + 8 + 2 * (lane & 3)]);
+            uint32_t w4[8];  // [value half][16-lane half's 8 rows][column block]
 #pragma unroll
-            for (int j = 0; j < NC / 8; ++j) {
-              o[2 * j] = pack_bf16(__uint_as_float(o[4 * j]) * inv[2 * j], __uint_as_float(o[4 * j + 1]) * inv[2 * j + 1]);
-              o[2 * j + 1] =
-                  pack_bf16(__uint_as_float(o[4 * j + 2]) * inv[2 * j], __uint_as_float(o[4 * j + 3]) * inv[2 * j + 1]);
+            for (int v = 0; v < 2; ++v) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int e = 8 * v + 2 * h;
+                w4[4 * v + h] = pack_bf16(__uint_as_float(o[e]) * i0.x, __uint_as_float(o[e + 1]) * i0.y);
+                w4[4 * v + 2 + h] = pack_bf16(__uint_as_float(o[e + 4]) * i1.x, __uint_as_float(o[e + 5]) * i1.y);
+              }
             }
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < NC / 16; ++j)
-              stmatrix_x4_trans(maddr + j * 512, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int v = 0; v < 2; ++v)
+              stmatrix_x4_trans(smem_u32(tb) + mcol * 64 + (((2 * v + mhalf) ^ ((mcol >> 1) & 3)) << 4), w4[4 * v],
+                                w4[4 * v + 1], w4[4 * v + 2], w4[4 * v + 3]);
             __syncwarp();
 #pragma unroll
-            for (int k = 0; k < NC / 16; ++k) {
-              const int col = k * 16 + (lane >> 1), half = lane & 1;
-              const uint4 v = *reinterpret_cast<const uint4*>(tb + col * 32 + ((half ^ ((col >> 2) & 1)) << 4));
-              if (cb + col < n)
-                *reinterpret_cast<uint4*>(oo + static_cast<int64_t>(col) * kLatent + (c >> 1) * 128 + (c & 1) * 16 +
-                                          half * 8) = v;
+            for (int k = 0; k < 2; ++k) {
+              const int col = k * 8 + (lane >> 2), part = lane & 3;
+              const uint4 v = *reinterpret_cast<const uint4*>(tb + col * 64 + ((part ^ ((col >> 1) & 3)) << 4));
+              const int cc = (c & 1) * 16 + col;
+              if (cb + cc < n)
+                *reinterpret_cast<uint4*>(oo + static_cast<int64_t>(cc) * kLatent + (c >> 1) * 128 + part * 8) = v;
             }
           }
         }
       } else {
         // [slot][value block, column half][column quad][value][column of the quad]
         float* po = p.part_o + (static_cast<int64_t>(slot) * 64 * 128 + quad * 32 + lane) * 4;
-#pragma unroll 1
-        for (int c = wg; c < 8; c += kSwg) {
-          if ((c & 1) * 32 >= n) continue;
-          uint32_t o[32];
+        // block t: values 128 (t / 2) + 32 quad + lane, columns 32 wg + 16 (t % 2) + {0 .. 15}
+        if (wg * 32 < n) {
+          uint32_t o[16], ahead[16];
           if (none) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0;
+            for (int k = 0; k < 16; ++k) ahead[k] = 0;
           } else {
-            tmem_ld32(tbase + kTmemO + c * 32 + lane_base, o);
-            tmem_ld_wait();
+            tmem_ld_x16(tbase + kTmemO + wg * 32 + lane_base, ahead);
           }
+#pragma unroll 1
+          for (int t = 0; t < 8; ++t) {
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if ((c & 1) * 32 + 4 * j < n)
-              *reinterpret_cast<uint4*>(po + (c * 8 + j) * 512) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int k = 0; k < 16; ++k) o[k] = ahead[k];
+            if (!none && t < 7)
+              tmem_ld_x16(tbase + kTmemO + ((t + 1) >> 1) * 64 + wg * 32 + ((t + 1) & 1) * 16 + lane_base, ahead);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (wg * 32 + (t & 1) * 16 + 4 * j < n)
+                *reinterpret_cast<uint4*>(po + (((t >> 1) * 2 + wg) * 8 + (t & 1) * 4 + j) * 512) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
         }
       }
       tc_fence_before();
@@ -1241,7 +1267,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_combine_kernel(const __gr
   __shared__ float4 wt[kJoinChunk][kAttnCols / 4];
   __shared__ float2 top_inv[kAttnCols];
   griddep_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   if (blockIdx.x == 0 && blockIdx.y == 0) collect_status(p);
   const int4 mt = p.meta[blockIdx.x];
   const int np = mt.y, x = blockIdx.x, vb = blockIdx.y;
@@ -1256,20 +1282,27 @@ __global__ void __launch_bounds__(kJoinThreads) latent_combine_kernel(const __gr
     acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (sub + 2 * u < quads) ahead[u] = piece_at(p, piece_slot(x, 0, p.ncg), vb, sub + 2 * u, val);
   }
-  for (int c = warp; c < n; c += kJoinThreads / 32) {
-    // one warp a column: the largest reference and the sum over all pieces
+  {
+    // four lanes a column: the largest reference and the sum over all pieces
+    const int c = tid >> 2, part = tid & 3;
     float top = -INFINITY, sum = 0.f;
-    for (int k = lane; k < np; k += 32) top = fmaxf(top, p.part_ml[piece_slot(x, k, p.ncg) * kAttnCols + c].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const float ref = top == -INFINITY ? 0.f : top;
-    for (int k = lane; k < np; k += 32) {
-      const float2 ml = p.part_ml[piece_slot(x, k, p.ncg) * kAttnCols + c];
-      sum = fmaf(ml.y, exp2f(ml.x - ref), sum);
+    if (c < n) {
+#pragma unroll 4
+      for (int k = part; k < np; k += 4) top = fmaxf(top, p.part_ml[piece_slot(x, k, p.ncg) * kAttnCols + c].x);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (lane == 0) {
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const float ref = top == -INFINITY ? 0.f : top;
+    if (c < n) {
+#pragma unroll 4
+      for (int k = part; k < np; k += 4) {
+        const float2 ml = p.part_ml[piece_slot(x, k, p.ncg) * kAttnCols + c];
+        sum = fmaf(ml.y, exp2f(ml.x - ref), sum);
+      }
+    }
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+    if (part == 0 && c < n) {
       top_inv[c] = make_float2(ref, sum == 0.f ? 0.f : 1.f / sum);
       if (vb == 0 && p.lse) p.lse[oc + c] = (top + log2f(sum)) * 0.69314718055994531f;
     }
