@@ -78,6 +78,10 @@ constexpr uint32_t kTmemO = 0;                  // four blocks of 128 values x 6
 constexpr uint32_t kTmemS = 256;                // two score buffers of 64 columns
 constexpr uint32_t kTmemPe = 384;               // fp8: the rotated part's scores, two buffers
 
+// What a CTA pays for a second segment (queries, first maxima, sums written
+// and joined), in tiles; and the even share above which it does not matter.
+constexpr int kSegmentTiles = 4, kGroupedTiles = 32;
+
 // A running maximum that grows by less than this many powers of two leaves
 // the sums as they are: weights may then reach 2^8, which bf16 and the fp32
 // sums hold with the same relative precision, and rescaling is rare.
@@ -108,7 +112,8 @@ struct Misc {
   int status;       // device status bits of this CTA
   int2 cut;         // (group, pieces) of the cut group whose first piece this CTA holds
   int scan[kMaxThreads / 32];
-  int start_group, start_tile;
+  int start_group, start_tile, end_tile, pieces;  // paged: where this CTA's range begins (and ends, with pieces > 0)
+  int tries[8];
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc");
 
@@ -356,7 +361,57 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
   // ---- this CTA's range of the tile axis
   bool too_long = false;
   int64_t total;
-  if (PAGED) {
+  // Paged: few requests with little work each get CTAs of their own, as many as
+  // a request takes at `tau` tiles each, so that no CTA has the end of one and
+  // the start of another (each segment costs about as much as kSegmentTiles
+  // tiles).  tau is the smallest of eight values from the even share on whose
+  // CTAs suffice; where it is more than the even share and a segment, the even
+  // ranges are the shorter ones.
+  const int even_of = p.parts, tries = 8;
+  auto tau_at = [&](int even, int u) {
+    const int tau0 = max(even, p.min_tiles);
+    return tau0 + u * max(1, tau0 / 8);
+  };
+  if (PAGED && p.groups <= 32) {
+    // a request a lane, in every warp alike: no barrier
+    const int L = lane < p.groups ? __ldg(p.seq_lens + lane) : 0;
+    too_long = L > p.max_blocks * kPageSize;
+    const int mine = lane < p.groups ? tiles_of(max(0, min(L, p.max_blocks * kPageSize))) : 0;
+    const int all = __reduce_add_sync(0xFFFFFFFFu, mine), even = (all + even_of - 1) / even_of;
+    total = all;
+    int tau = 0;
+    if (p.groups <= p.parts && even <= kGroupedTiles) {
+#pragma unroll 1
+      for (int u = 0; u < tries && tau == 0; ++u) {
+        const int v = tau_at(even, u);
+        if (v > max(even + kSegmentTiles, p.min_tiles)) break;
+        if (static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, (mine + v - 1) / v)) <= p.parts) tau = v;
+      }
+    }
+    // the requests' shares of the CTAs, or of the tile axis
+    const int c = tau > 0 ? (mine + tau - 1) / tau : mine;
+    int pre = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, pre, d);
+      if (lane >= d) pre += v;
+    }
+    const int64_t parts = min(static_cast<int64_t>(p.parts), total);
+    const int x = tau > 0 ? part : part < parts ? static_cast<int>(part * total / parts) : all;
+    if (warp == 0) {
+      if (lane == 0) ms.pieces = tau > 0 ? 0 : -1;
+      __syncwarp();
+      if (x >= pre - c && x < pre) {
+        const int r = x - (pre - c);
+        ms.start_group = lane;
+        ms.start_tile = tau > 0 ? static_cast<int>(static_cast<int64_t>(r) * mine / c) : r;
+        if (tau > 0) {
+          ms.end_tile = static_cast<int>(static_cast<int64_t>(r + 1) * mine / c);
+          ms.pieces = c;
+        }
+      }
+    }
+  } else if (PAGED) {
     // prefix sum over the requests: each thread a contiguous run of them
     const int per = (p.groups + kThreads - 1) / kThreads;
     const int g0 = min(tid * per, p.groups), g1 = min(g0 + per, p.groups);
@@ -365,32 +420,62 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       mine += tiles_of(group_len<true>(p, g));
       too_long = too_long || __ldg(p.seq_lens + g) > p.max_blocks * kPageSize;
     }
-    int inc = mine;
+    auto scan = [&](int v) {  // inclusive, over the block
+      int inc = v;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-      if (lane >= d) inc += v;
-    }
-    if (lane == 31) ms.scan[warp] = inc;
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += ms.scan[w];
-      all += ms.scan[w];
-    }
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      if (lane == 31) ms.scan[warp] = inc;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) inc += ms.scan[w];
+      return inc;
+    };
+    const int inc = scan(mine);
+    int all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) all += ms.scan[w];
     total = all;
-    const int64_t parts = min(static_cast<int64_t>(p.parts), total);
-    const int64_t x = part < parts ? part * total / parts : total;
-    int at = before + inc - mine;  // the run's first tile
-    if (x >= at && x < at + mine) {
-      for (int g = g0; g < g1; ++g) {
-        const int n = tiles_of(group_len<true>(p, g));
-        if (x < at + n) {
-          ms.start_group = g;
-          ms.start_tile = static_cast<int>(x - at);
-          break;
+    const int even = (all + even_of - 1) / even_of;
+    int tau = 0;
+    if (p.groups <= min(p.parts, kThreads) && even <= kGroupedTiles) {
+      if (tid < tries) ms.tries[tid] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < tries; ++u) {
+        const int v = tau_at(even, u), c = __reduce_add_sync(0xFFFFFFFFu, (mine + v - 1) / v);
+        if (lane == 0) atomicAdd(&ms.tries[u], c);
+      }
+      __syncthreads();
+      for (int u = tries - 1; u >= 0; --u)
+        if (ms.tries[u] <= p.parts) tau = tau_at(even, u);
+      if (tau > max(even + kSegmentTiles, p.min_tiles)) tau = 0;
+    }
+    if (tau > 0) {
+      const int c = (mine + tau - 1) / tau;
+      if (tid == 0) ms.pieces = 0;
+      const int r = part - (scan(c) - c);
+      if (r >= 0 && r < c) {
+        ms.start_group = tid;
+        ms.start_tile = static_cast<int>(static_cast<int64_t>(r) * mine / c);
+        ms.end_tile = static_cast<int>(static_cast<int64_t>(r + 1) * mine / c);
+        ms.pieces = c;
+      }
+    } else {
+      if (tid == 0) ms.pieces = -1;
+      const int64_t parts = min(static_cast<int64_t>(p.parts), total);
+      const int64_t x = part < parts ? part * total / parts : total;
+      int at = inc - mine;  // the run's first tile
+      if (x >= at && x < at + mine) {
+        for (int g = g0; g < g1; ++g) {
+          const int n = tiles_of(group_len<true>(p, g));
+          if (x < at + n) {
+            ms.start_group = g;
+            ms.start_tile = static_cast<int>(x - at);
+            break;
+          }
+          at += n;
         }
-        at += n;
       }
     }
   } else {
@@ -402,6 +487,10 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
   const int64_t parts = min(static_cast<int64_t>(p.parts), total);
   int64_t x0 = part < parts ? part * total / parts : 0;
   int64_t x1 = part < parts ? (part + 1) * total / parts : 0;
+  if (PAGED && ms.pieces >= 0) {  // a request's own CTAs
+    x0 = 0;
+    x1 = ms.pieces > 0 ? ms.end_tile - ms.start_tile : 0;
+  }
   if (!PAGED && p.whole_groups) {  // ranges that end with groups
     x0 = static_cast<int64_t>(part) * p.groups / p.parts * tiles_of(p.topk);
     x1 = static_cast<int64_t>(part + 1) * p.groups / p.parts * tiles_of(p.topk);
@@ -448,9 +537,12 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       fresh = true;
       if (t == 0 && te < nt && pt == 0) {
         // the group goes on in the ranges after this one, up to the one that holds its last tile
-        const int64_t last = x1 - left + nt - 1;
-        const int c1 = static_cast<int>(((last + 1) * parts - 1) / total);
-        ms.cut = make_int2(g, c1 - part + 1);
+        int pieces = PAGED ? ms.pieces : 0;
+        if (pieces <= 0) {
+          const int64_t last = x1 - left + nt - 1;
+          pieces = static_cast<int>(((last + 1) * parts - 1) / total) - part + 1;
+        }
+        ms.cut = make_int2(g, pieces);
       }
       from_start = t == 0;
       if (t == 0 && pt == 0 && p.groups <= kSpreadGroups)

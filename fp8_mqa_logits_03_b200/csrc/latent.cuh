@@ -61,6 +61,7 @@ struct LatentAttnParams {
   // schedule: the groups' tiles back to back, cut into `parts` equal ranges;
   // CTA x takes column block x % ncg of range x / ncg
   int ncg, parts;
+  int min_tiles;            // tiles a range holds at least, where there are that many
   int whole_groups;         // selected form: ranges end with groups, none is cut
   int* status;
   float* part_o;            // [grid][2][64 x 512] unnormalised sums of cut groups

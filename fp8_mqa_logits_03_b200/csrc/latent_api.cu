@@ -31,6 +31,7 @@ int sms_cached() {
 
 struct AttnPlan {
   int ncg = 1, parts = 1;
+  int min_tiles = 1;
   bool whole_groups = false;
   size_t off_meta = 0, off_group = 0, off_ml = 0, off_o = 0, total = 0;
 };
@@ -43,18 +44,25 @@ constexpr int64_t kJoinTiles = 4;
 // in L2) and as many ranges of the tile axis as fit; a range holds at least
 // one tile.  Where all groups have the same number of tiles (`uniform`), the
 // ranges end with groups if that makes the longest one at most kJoinTiles
-// longer: nothing is then left to be joined.
+// longer: nothing is then left to be joined; or else, under the same
+// condition, every group gets ranges of its own.
 AttnPlan plan_attn(int64_t groups, int64_t cols, int64_t tiles_per_group, bool uniform, int sms) {
   AttnPlan pl;
   pl.ncg = static_cast<int>(ceil_div(cols, kAttnCols));
   const int64_t nt = std::max<int64_t>(1, tiles_per_group);
   const int64_t tiles = std::max<int64_t>(1, groups * nt);
-  pl.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / pl.ncg, tiles, kAttnMaxParts})));
+  // a cut range leaves cols x 2 KB of sums: with many columns as much as some tiles
+  pl.min_tiles = cols > 32 ? 2 : 1;
+  const int64_t slots = std::max<int64_t>(1, std::min<int64_t>(sms / pl.ncg, kAttnMaxParts));
+  pl.parts = static_cast<int>(std::min<int64_t>(slots, ceil_div(tiles, pl.min_tiles)));
   if (uniform && groups > 0) {
-    const int64_t most = std::min<int64_t>(pl.parts, groups), each = ceil_div(groups, most);
-    if (each * nt <= ceil_div(tiles, pl.parts) + kJoinTiles) {
+    const int64_t even = ceil_div(tiles, pl.parts), most = std::min<int64_t>(pl.parts, groups);
+    const int64_t each = ceil_div(groups, most), split = std::max<int64_t>(1, pl.parts / groups);
+    if (each * nt <= even + kJoinTiles) {
       pl.whole_groups = true;
       pl.parts = static_cast<int>(ceil_div(groups, each));
+    } else if (groups <= pl.parts && ceil_div(nt, split) <= even + kJoinTiles) {
+      pl.parts = static_cast<int>(groups * split);  // a group's own ranges: none holds parts of two
     }
   }
   const int64_t grid = static_cast<int64_t>(pl.parts) * pl.ncg;
@@ -110,6 +118,7 @@ int run_attn(LatentAttnParams& p, const AttnPlan& pl, bool paged, bool fp8, void
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.ncg = pl.ncg;
   p.parts = pl.parts;
+  p.min_tiles = pl.min_tiles;
   p.whole_groups = pl.whole_groups ? 1 : 0;
   p.group_meta = reinterpret_cast<int2*>(wsb + pl.off_group);
   p.status = reinterpret_cast<int*>(wsb);
