@@ -102,7 +102,8 @@ struct Misc {
   uint64_t empty[kStages][kParts];
   uint64_t q_full;
   uint64_t s_full[2], s_empty[2];
-  uint64_t p_full, pv_done, drain;
+  uint64_t p_full[2], pv_done[2];  // by tile parity: a wait for a tile never meets the phase of another
+  uint64_t drain;
   Info info[kInfo];
   float scale[2][3][kAttnKeys];  // fp8: the tile's key scales s, log2 s and 1 / s, by tile parity
   float q_scale[2][kAttnCols];   // fp8: what a column's scores are multiplied by (log2 units)
@@ -148,23 +149,9 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
-// 16 lanes x 64 (or 32, 16) columns: thread t receives, for each 8-column block j, columns
+// 16 lanes x 16 (or 32) columns: thread t receives, for each 8-column block j, columns
 // 8j + 2(t % 4) + {0, 1} of lane t / 4 in r[4j], r[4j+1] and of lane t / 4 + 8
 // in r[4j+2], r[4j+3].
-__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -342,9 +329,9 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ms.s_full[b], 1);
       mbar_init(&ms.s_empty[b], kSoftmax);
+      mbar_init(&ms.p_full[b], kSoftmax);
+      mbar_init(&ms.pv_done[b], 1);
     }
-    mbar_init(&ms.p_full, kSoftmax);
-    mbar_init(&ms.pv_done, 1);
     mbar_init(&ms.drain, 2);
     ms.abort_flag = 0;
     ms.status = 0;
@@ -714,7 +701,9 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const bool null = flags & (kNull | kEnd);
       if ((flags & kFirst) && !null && i > 0) {
         // ---- the group's query columns; their place is free once the scores of tile i - 1 are done
-        if (!warp_wait(&ms.empty[st ^ 1][4], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) break;
+        // (and of tile i - 2: a tile i - 1 without keys has none)
+        if (!warp_wait(&ms.s_full[st ^ 1], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) break;
+        if (i > 1 && !warp_wait(&ms.s_full[st], ph ^ 1, abort_flag, &ms.status, limit)) break;
         copy_q(d.group);
       }
       if (i == 0 && null) cp_async_wait_all();  // the queries copied ahead are not used: out of the way of the next ones
@@ -739,37 +728,33 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       if (FP8 && !null) {
         // The codes land in the first half of the stage, and the rotated part,
         // bf16 as it is, in its place.  The second half's codes become fp16 in
-        // the second half; then every thread takes the others that it copied
-        // into registers, and when all have, they become fp16 in the first.
-        if (!warp_wait(&ms.empty[st][1], ph ^ 1, abort_flag, &ms.status, limit)) break;
+        // the second half; then the others, two rows at a time into registers
+        // and from there, as fp16, into the first.
         const uint32_t land = dst + swz;
         if (pt < kAttnKeys) cp_async4(smem_u32(&ms.scale[st][0][pt]), p.s + max(key_slot, 0), key_slot >= 0 ? 4 : 0);
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const uint8_t* at = row_at(row[k]);
-          const uint32_t n = row[k] >= 0 ? 16 : 0;
-          cp_async16(land + 2 * kChunkBytes + k * (kRows * 128), at + 2 * 128, n);
-          cp_async16(land + 3 * kChunkBytes + k * (kRows * 128), at + 3 * 128, n);
-        }
-        cp_async_commit();
+        for (int c = 0; c < 2; ++c) {  // the second half's codes into part 0, the first half's into part 1
+          if (c == 1 && !warp_wait(&ms.empty[st][1], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const uint8_t* at = row_at(row[k]);
-          const uint32_t n = row[k] >= 0 ? 16 : 0;
-          cp_async16(land + k * (kRows * 128), at, n);
-          cp_async16(land + kChunkBytes + k * (kRows * 128), at + 128, n);
+          for (int k = 0; k < NK; ++k) {
+            const uint8_t* at = row_at(row[k]) + (c == 0 ? 256 : 0);
+            const uint32_t n = row[k] >= 0 ? 16 : 0;
+            cp_async16(land + 2 * c * kChunkBytes + k * (kRows * 128), at, n);
+            cp_async16(land + (2 * c + 1) * kChunkBytes + k * (kRows * 128), at + 128, n);
+          }
+          cp_async_commit();
         }
-        cp_async_commit();
-        if (!warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit)) break;
+        if (!ok) break;
+        if (!warp_wait(&ms.empty[st][2], ph ^ 1, abort_flag, &ms.status, limit) ||
+            !warp_wait(&ms.empty[st][3], ph ^ 1, abort_flag, &ms.status, limit) ||
+            !warp_wait(&ms.empty[st][4], ph ^ 1, abort_flag, &ms.status, limit))
+          break;
 #pragma unroll
         for (int k = 0; k < NK; ++k)
           cp_async16(land + 8 * kChunkBytes + k * (kRows * 128),
                      p.pe + static_cast<int64_t>(max(row[k], 0)) * (kRope * 2) + piece * 16, row[k] >= 0 ? 16 : 0);
         cp_async_arrive(&ms.full[st][2]);
         cp_async_commit();
-        if (!warp_wait(&ms.empty[st][2], ph ^ 1, abort_flag, &ms.status, limit) ||
-            !warp_wait(&ms.empty[st][3], ph ^ 1, abort_flag, &ms.status, limit))
-          break;
         cp_async_wait<2>();
         if (pt < kAttnKeys) {
           // a scale of 0 (or below 2^-60, or of a key that does not exist)
@@ -783,20 +768,20 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         for (int c = 2; c < 4; ++c)
 #pragma unroll
           for (int k = 0; k < NK; ++k)
-            store_codes(ld_shared16(land + c * kChunkBytes + k * (kRows * 128)), c, k, dst);
+            store_codes(ld_shared16(land + (c - 2) * kChunkBytes + k * (kRows * 128)), c, k, dst);
         __syncwarp();
         if (lane == 0 && !withhold) mbar_arrive(&ms.full[st][0]);
         cp_async_wait<1>();
-        uint4 raw[2 * NK];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int k = 0; k < NK; k += 2) {
+          uint4 raw[4];
 #pragma unroll
-          for (int k = 0; k < NK; ++k) raw[NK * c + k] = ld_shared16(land + c * kChunkBytes + k * (kRows * 128));
-        named_bar_sync(3, kProducers);
+          for (int u = 0; u < 4; ++u)
+            raw[u] = ld_shared16(land + (2 + (u & 1)) * kChunkBytes + (k + (u >> 1)) * (kRows * 128));
+          __syncwarp();  // (a row's eight pieces are one warp's, landing and converted)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int k = 0; k < NK; ++k) store_codes(raw[NK * c + k], c, k, dst);
+          for (int u = 0; u < 4; ++u) store_codes(raw[u], u & 1, k + (u >> 1), dst);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.full[st][1]);
       } else if (FP8) {
@@ -857,7 +842,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           ok = warp_wait(&ms.full[st][c], ph, abort_flag, &ms.status, limit);
         if (!ok) break;
         if (elect_one()) {
-          if (!(flags & kEnd)) mbar_arrive(&ms.empty[st][4]);
           mbar_arrive(&ms.s_full[st]);
         }
         __syncwarp();
@@ -887,10 +871,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
                      ks > 0 || (c != Sh::first_part(0) && !(FP8 && c == 4)));
             }
           }
-          if (f == Sh::kFull - 1) {
-            mma_commit(&ms.empty[st][4]);
-            mma_commit(&ms.s_full[st]);
-          }
+          if (f == Sh::kFull - 1) mma_commit(&ms.s_full[st]);
         }
         __syncwarp();
       }
@@ -901,29 +882,32 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
   } else if (warp == kValueWarp) {
     // ================================================================ value products
     constexpr uint32_t id_v = idesc_16_f32(128, 64, true, FP8);
-    const uint64_t p_d = smem_desc_k128_sw128(smem_u32(smem + kOffP));
     for (int i = 0;; ++i) {
       const int st = i & 1;
-      if (!warp_wait(&ms.p_full, i & 1, abort_flag, &ms.status, limit)) break;
+      if (!warp_wait(&ms.p_full[st], (i >> 1) & 1, abort_flag, &ms.status, limit)) break;
       const int flags = ms.info[i & (kInfo - 1)].flags;
       if (flags & kEnd) break;
       tc_fence_after();
       if (elect_one()) {
         if (flags & kNull) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mbar_arrive(&ms.empty[st][c]);
-          mbar_arrive(&ms.pv_done);
+          for (int c = 0; c < kParts - 1; ++c) mbar_arrive(&ms.empty[st][c]);
+          mbar_arrive(&ms.pv_done[st]);
+          mbar_arrive(&ms.empty[st][4]);
         } else {
           const uint64_t v_d = smem_desc_mn_sw128(smem_u32(smem + kOffK + st * kStageBytes));
+          const uint64_t p_d = smem_desc_k128_sw128(smem_u32(smem + kOffK + st * kStageBytes + 8 * kChunkBytes));
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma_16(tbase + kTmemO + c * 64, v_d + ((2 * c * kChunkBytes + ks * 2048) >> 4), p_d + ks * 2, id_v,
                        ks > 0 || !(flags & kFirst));
-            mma_commit(&ms.empty[st][c]);
+            if (c < 3) mma_commit(&ms.empty[st][c]);
           }
-          mma_commit(&ms.pv_done);
+          mma_commit(&ms.pv_done[st]);  // no later than the stage's last release
+          mma_commit(&ms.empty[st][3]);
+          mma_commit(&ms.empty[st][4]);  // (the weights lie in the rotated part's place)
         }
       }
       __syncwarp();
@@ -947,7 +931,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     // exchanged between the two warpgroups in the weights' buffer, while no weights are in it
     float* half_max = reinterpret_cast<float*>(smem + kOffP);
     float* stat_l1 = half_max;
-    uint8_t* prow = smem + kOffP + rr * 128 + 4 * (lane & 3);
+    uint8_t* prow = smem + kOffK + 8 * kChunkBytes + rr * 128 + 4 * (lane & 3);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float to_log2[2] = {p.scale_log2, p.scale_log2};
     bool dead = false;
@@ -1083,8 +1067,9 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       auto put_weights = [&]() {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          *reinterpret_cast<uint32_t*>(prow + (((wg * NJ + j) ^ (rr & 7)) << 4)) = w[2 * j];
-          *reinterpret_cast<uint32_t*>(prow + 8 * 128 + (((wg * NJ + j) ^ (rr & 7)) << 4)) = w[2 * j + 1];
+          uint8_t* at = prow + b * kStageBytes + (((wg * NJ + j) ^ (rr & 7)) << 4);
+          *reinterpret_cast<uint32_t*>(at) = w[2 * j];
+          *reinterpret_cast<uint32_t*>(at + 8 * 128) = w[2 * j + 1];
         }
       };
       const bool live = !(flags & (kNull | kEnd));
@@ -1099,6 +1084,8 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       for (int pass = 0; pass < 2; ++pass) {
         if (live && (pass == 1 || !(flags & kFirst))) read_scores();
         if (pass == 1) {
+          // (the sums hold still once the previous value product is done)
+          if (i > 0 && !warp_wait(&ms.pv_done[b ^ 1], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) dead = true;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
@@ -1143,8 +1130,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         }
         const bool weighs = live && (pass == 1 || !(flags & kFirst));
         if (weighs) weigh();
-        // the previous value product is done: the weights' buffer is free and the sums hold still
-        if (pass == 0 && i > 0 && !warp_wait(&ms.pv_done, (i - 1) & 1, abort_flag, &ms.status, limit)) dead = true;
         if (weighs) put_weights();
         if (pass == 1) break;
         const bool grow = mx[0] > m[0] + kRescaleLog2 || mx[1] > m[1] + kRescaleLog2;
@@ -1156,7 +1141,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         if (!live || !(vote || (flags & kFirst))) break;
       }
       if (leave) {
-        mbar_arrive(&ms.p_full);  // the value warp sees the end too
+        mbar_arrive(&ms.p_full[b]);  // the value warp sees the end too
         break;
       }
       if (!dead) {
@@ -1169,14 +1154,16 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         fence_async_shared();
       }
       tc_fence_before();
-      mbar_arrive(&ms.p_full);
+      mbar_arrive(&ms.p_full[b]);
       if (!(flags & kLast)) continue;
 
       // ---- the segment's end: its sums, divided (a whole group) or as they are (a cut one)
       const int group = f.group, slot = f.piece;
       const bool none = (flags & kNull) && (flags & kFirst);  // no key at all: the sums were never written
       const bool direct = flags & kDirect;
-      if (!warp_wait(&ms.pv_done, i & 1, abort_flag, &ms.status, limit)) dead = true;
+      // (a last tile without keys is done at once, the one before it perhaps not)
+      if (i > 0 && !warp_wait(&ms.pv_done[b ^ 1], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) dead = true;
+      if (!warp_wait(&ms.pv_done[b], (i >> 1) & 1, abort_flag, &ms.status, limit)) dead = true;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);

@@ -464,6 +464,57 @@ def test_offsets_past_32_bits():
     assert torch.equal(kv.view(-1, 576)[-1], x[0])
 
 
+def _ragged_lengths(B, top, seed):
+    """Lengths from 0 to `top`, the longest and the shortest among them."""
+    g = np.random.default_rng(seed)
+    l = g.integers(0, top + 1, B)
+    l[g.integers(0, B)], l[g.integers(0, B)] = top, 0
+    return [int(v) for v in l]
+
+
+# how the requests are shared out depends on their number (a lane or a thread
+# each, or several a thread) and on whether each can have CTAs of its own
+@pytest.mark.parametrize("B,top,R,H", [(12, 900, 2, 16), (32, 400, 1, 64), (33, 500, 1, 40), (20, 4000, 1, 8), (5, 6000, 8, 128), (147, 200, 1, 24),
+                                       (150, 130, 1, 64), (460, 100, 3, 4), (600, 70, 1, 3)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_paged_many_requests(B, top, R, H, fp8):
+    lengths = _ragged_lengths(B, top, 380 + B)
+    dev, keys, table, q, qn = _paged_case(lengths, R, H, fp8, 381 + B)
+    out, lse = fx.paged_latent_attention(q, block_table=torch.from_numpy(table).cuda(),
+                                         seq_lens=torch.tensor(lengths, dtype=torch.int32).cuda(), R=R, scale=SCALE, **dev,
+                                         return_lse=True)
+    out, lse = _np(out), _np(lse)
+    order = np.argsort(lengths)
+    for b in sorted({0, 1, B // 2, B - 2, B - 1, int(order[0]), int(order[1]), int(order[-1]), *range(0, B, max(1, B // 12))}):
+        at = _logical(table, b, lengths[b])
+        for t in range(R):
+            i = b * R + t
+            _check_row(out[i], lse[i], qn[i], keys[at[:max(0, lengths[b] - R + t + 1)]], fp8, f"request {b} row {t}")
+
+
+# ranges that end with rows (many of them), rows with CTAs of their own, cut rows; one and two column blocks
+@pytest.mark.parametrize("rows,H,topk,counts", [(3, 128, 2048, None), (40, 64, 2048, None), (148, 64, 320, (320, 1, 256, 0, 64)),
+                                                (500, 64, 320, (320, 1, 256, 0, 64)), (9, 16, 4096, None), (600, 100, 192, None)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sparse_same_bits_in_many_runs(rows, H, topk, counts, fp8):
+    """Calls back to back on the same inputs: a missing wait shows as a run that
+    differs.  A sample of the rows is checked too."""
+    pages = 64
+    dev, keys = _pool(pages, fp8, 390 + rows)
+    q, qn = _q(rows, H, 391)
+    sln = _slots(rows, topk, pages * 64, 392, counts)
+    sl = torch.from_numpy(sln).cuda()
+    out, lse = fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev, return_lse=True)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        o, l = fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev, return_lse=True)
+        wrong += (o != out).any() | (l != lse).any()
+    assert wrong.item() == 0
+    o, l = _np(out), _np(lse)
+    for i in range(0, rows, max(1, rows // 10)):
+        _check_row(o[i], l[i], qn[i], keys[sln[i][sln[i] >= 0]], fp8, f"row {i}")
+
+
 # ------------------------------------------------------------------ how it is called
 
 def _args(fp8, rows=5, H=24, topk=300, seed=400):
