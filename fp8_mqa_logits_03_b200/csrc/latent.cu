@@ -881,7 +881,8 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     __syncwarp();
   } else if (warp == kValueWarp) {
     // ================================================================ value products
-    constexpr uint32_t id_v = idesc_16_f32(128, 64, true, FP8);
+    // (as many columns as there are, in sixteens: the sums of the others are never read)
+    const uint32_t id_v = idesc_16_f32(128, (min(kAttnCols, p.R * p.H - cg * kAttnCols) + 15) & ~15, true, FP8);
     for (int i = 0;; ++i) {
       const int st = i & 1;
       if (!warp_wait(&ms.p_full[st], (i >> 1) & 1, abort_flag, &ms.status, limit)) break;
