@@ -11,27 +11,41 @@
 // sees keys [0, L - R + t + 1)).
 //
 // Work is cut into units of 64 columns of one group (a query row, or a
-// request's R x H columns) times tiles of 64 keys.  The groups' tiles lie back
-// to back on one axis, which is cut into equal ranges, one per CTA: every SM
-// gets the same number of tiles whatever the groups' lengths.  A group that
-// lies inside one range is written directly; one that is cut leaves partial
-// sums, which combine_kernel joins in order.
+// request's R x H columns) times tiles of 64 keys (a page).  The groups' tiles
+// lie back to back on one axis, which is cut into ranges, one per CTA: equal
+// ones, so that every SM gets the same number of tiles whatever the groups'
+// lengths, or, where that costs little, ranges that end with groups (selected
+// form) or shares of a group's own (few, short ones).  A group that lies
+// inside one range is written directly; one that is cut leaves partial sums
+// in 32 bits, which latent_combine_kernel or latent_spread_kernel joins in
+// key order: the same bits every time.
 //
-// One CTA, warp-specialised:
-//   warps 0-3  softmax: read the 64 x 64 scores from TMEM (16 heads a warp,
-//              four lanes a head), running maximum and sum in registers,
-//              weights as bf16 into shared memory; at a group's end they read
-//              the sums from TMEM, divide and write.
-//   four warps producers: gather the tile's key rows into one of
-//              two stages in the 128-byte swizzle.  bf16: 16-byte
-//              asynchronous copies.  fp8: the codes land in one half of the
-//              stage and become fp16 in its whole, exactly; the scales go to
-//              the softmax warps.
-//   two more   one issues the score products, part by part as a tile lands,
-//   warps      the other the value products.
+// One CTA per SM, warp-specialised (448 threads, 227 KB of shared memory):
+//   eight warps  softmax: warpgroup w has keys [32 w, 32 w + 32) of a tile,
+//                each warp 16 columns of them, four lanes a column.  Scores
+//                come from TMEM, running maximum and sum stay in registers,
+//                weights go to shared memory; at a segment's end they read
+//                the sums from TMEM, divide and write.
+//   four warps   producers: gather the tile's key rows into one of two stages
+//                in the 128-byte swizzle.  bf16: 16-byte asynchronous copies.
+//                fp8: the codes land in one half of the stage and become fp16
+//                in its whole, exactly; the rotated part stays bf16.
+//   two warps    one issues the score products, part by part as a tile lands,
+//                the other the value products.
 // Scores: M = 64 columns, N = 64 keys, K = 576.  Values, transposed so that
 // the sums of all 512 values fit in half of TMEM: M = 128 values (the same
-// key rows read as an MN-major operand), N = 64 columns, K = 64 keys.
+// key rows read as an MN-major operand), N = 64 columns, K = 64 keys.  The
+// weights take the place of the rotated part, which only the scores read.
+//
+// What bounds it: shared memory's 128 bytes a cycle.  A tile's score products
+// read 36 x 4 KB (measured: 33 cycles each), its value products 16 x 6 KB (49
+// cycles), its keys are written once, 72 KB: 2500 cycles.  4096 rows x 64
+// heads x 2048 bf16 keys take 1.46 ms (800 TFLOP/s), 2980 cycles a tile with
+// the segments' starts and ends; fp8 codes are written, read and written again
+// (another 64 KB) and take about 4000 (1024 rows x 128 heads: 0.98 ms).  Stages of 64 keys are the largest of which two fit beside
+// the queries; over one tile or two, waits for memory and hand-overs count:
+// one row of 16 heads x 2048 keys, a tile a CTA, takes 10.7 us.  Long
+// contexts with 64 columns a request reach 5.4 TB/s of keys.
 #include <cstdint>
 
 #include "kernels.cuh"
@@ -80,6 +94,7 @@ constexpr uint32_t kTmemPe = 384;               // fp8: the rotated part's score
 
 // What a CTA pays for a second segment (queries, first maxima, sums written
 // and joined), in tiles; and the even share above which it does not matter.
+// (7 requests x 3 rows of up to 5000 fp8 keys: 39 us in even ranges, 31 in own ones.)
 constexpr int kSegmentTiles = 4, kGroupedTiles = 32;
 
 // A running maximum that grows by less than this many powers of two leaves

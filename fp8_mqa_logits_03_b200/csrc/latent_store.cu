@@ -14,7 +14,11 @@
 // heads [16 g, 16 g + 16).  A vector of 64 values takes four lanes, eight
 // pairs each, so a lane's eight cosines and sines are loaded once for all
 // heads of the warp; all of a warp's loads are issued before any arithmetic.
-// The kernel is a plain HBM stream.
+// A plain HBM stream without reuse: 8192 tokens with 64 heads into an fp8 pool
+// (151 MB) take 30.3 us, 5.0 TB/s; 256 tokens with 16 heads 1.9 us, a launch.
+// The large case is bound by DRAM's 128-byte runs (a head's rotary part lies
+// 384 bytes from the next, its place in the queries 1152): 2 or 8 warps a CTA,
+// and loads before the checks of position and slot, all take 30.3 us too.
 #include <cstdint>
 
 #include "kernels.cuh"

@@ -304,8 +304,10 @@ int fp8idx_latent_store(const uint16_t* c, int64_t c_stride, const uint16_t* k_p
  * A row without slots gives 0 and -inf.  A slot named twice counts twice.
  * Negative entries are skipped wherever they stand; a slot at or past
  * num_slots is left out and sets BAD_SLOT.  The products are exact with fp32
- * sums; the softmax weights are rounded to bf16 for the value product, the
- * sum that divides them is not.
+ * sums; the softmax weights are rounded for the value product, to bf16 (bf16
+ * pool) or, with the key's scale in them, to fp16 (fp8 pool); the sum that
+ * divides them is not.  fp8 pool: scales are not negative, and one below
+ * 2^-60 (0 included) counts as 2^-60 where its key's weight is formed.
  *   q          [rows, H, 576] bf16, row and head strides in values (multiples
  *              of 16 bytes), H in [1, 128]; latent must be 512 and rope 64
  *   pool       as fp8idx_latent_store, num_slots < 2^31
