@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -113,10 +114,29 @@ T* as(const at::Tensor& t) {
   return static_cast<T*>(ptr(t));
 }
 
-// The stream of the call: the caller's (a pointer as an int), or the current one of the device.
-void* stream_of(PyObject* o, const at::Tensor& t) {
-  if (o != Py_None) return PyLong_AsVoidPtr(o);
-  return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+// Makes the call's device current, and its stream, if the caller names one (a
+// pointer as an int): the outputs and the workspace that the call makes are
+// then that stream's, as under torch.cuda.stream, and the allocator does not
+// hand the workspace to another stream while the call still uses it.
+struct OnStream {
+  c10::cuda::OptionalCUDAGuard device;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  void* stream;
+  OnStream(PyObject* o, const at::Tensor& t) : device(t.device()) {
+    if (o != Py_None)
+      guard.reset_stream(
+          c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(PyLong_AsVoidPtr(o)), t.device().index()));
+    stream = c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+  }
+};
+
+// The stride of a dimension; one of size 1 has none that matters.
+int64_t row_stride(const at::Tensor& t, int64_t d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+
+// The calls have no backward pass: a gradient must not be lost in silence.
+void no_grad(const at::Tensor& t, const char* name) {
+  if (t.defined() && t.requires_grad() && c10::GradMode::is_enabled())
+    throw ValueError(std::string(name) + " requires grad, and this call has no backward: detach it or call under torch.no_grad()");
 }
 
 struct Outputs {
@@ -212,15 +232,20 @@ PyObject* latent_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (qi.sizes() != qo.sizes() || qi.size(0) != T) throw ValueError("q_pe and q_out must be [T, H, 64]");
       same_device(p.kv, qi, "q_pe");
       same_device(p.kv, qo, "q_out");
-      s[0] = qi.stride(0), s[1] = qi.stride(1), s[2] = qo.stride(0), s[3] = qo.stride(1);
+      s[0] = row_stride(qi, 0), s[1] = row_stride(qi, 1), s[2] = row_stride(qo, 0), s[3] = row_stride(qo, 1);
+      no_grad(qi, "q_pe");
+      no_grad(qo, "q_out");
       H = qi.size(1);
     }
     const int interleaved = PyObject_IsTrue(a[10]);
-    const c10::cuda::OptionalCUDAGuard g(p.kv.device());
-    return PyLong_FromLong(f_store(as<uint16_t>(c), c.stride(0), as<uint16_t>(k_pe), k_pe.stride(0), T, as<int64_t>(pos),
+    no_grad(c, "c");
+    no_grad(k_pe, "k_pe");
+    no_grad(p.kv, "kv_pages");
+    const OnStream on(a[11], p.kv);
+    return PyLong_FromLong(f_store(as<uint16_t>(c), row_stride(c, 0), as<uint16_t>(k_pe), row_stride(k_pe, 0), T, as<int64_t>(pos),
                                    as<float>(cs), cs.size(0), interleaved, as<int64_t>(slot), p.pages * kPage,
                                    ptr(p.kv), as<float>(p.s), as<uint16_t>(p.pe), as<uint16_t>(qi), s[0], s[1],
-                                   as<uint16_t>(qo), s[2], s[3], static_cast<int>(H), stream_of(a[11], p.kv)));
+                                   as<uint16_t>(qo), s[2], s[3], static_cast<int>(H), on.stream));
   });
 }
 
@@ -240,14 +265,16 @@ PyObject* sparse_latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const double scale = PyFloat_AsDouble(a[3]);
     if (PyErr_Occurred()) return nullptr;
     const bool want_lse = PyObject_IsTrue(a[9]);
-    const c10::cuda::OptionalCUDAGuard g(q.device());
+    no_grad(q, "q");
+    no_grad(p.kv, "kv_pages");
+    const OnStream on(a[10], q);
     const Outputs o = outputs(q, a[6], a[7], want_lse);
     const at::Tensor ws = workspace_of(q, a[8], f_sparse_ws(nr, static_cast<int>(H), static_cast<int>(topk)));
     const int64_t ld = nr <= 1 || topk == 0 ? topk : slots.stride(0);
-    return results(f_sparse(as<uint16_t>(q), q.stride(0), q.stride(1), ptr(p.kv), as<float>(p.s), as<uint16_t>(p.pe),
+    return results(f_sparse(as<uint16_t>(q), row_stride(q, 0), row_stride(q, 1), ptr(p.kv), as<float>(p.s), as<uint16_t>(p.pe),
                             p.pages * p.page, as<int32_t>(slots), ld, nr, static_cast<int>(topk), static_cast<int>(H),
                             kLatent, kRope, static_cast<float>(scale), as<uint16_t>(o.out), as<float>(o.lse), ptr(ws),
-                            ws.numel(), stream_of(a[10], q)),
+                            ws.numel(), on.stream),
                    o, want_lse);
   });
 }
@@ -271,14 +298,16 @@ PyObject* paged_latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(q, bt, "block_table");
     same_device(q, sl, "seq_lens");
     const bool want_lse = PyObject_IsTrue(a[11]);
-    const c10::cuda::OptionalCUDAGuard g(q.device());
+    no_grad(q, "q");
+    no_grad(p.kv, "kv_pages");
+    const OnStream on(a[12], q);
     const Outputs o = outputs(q, a[8], a[9], want_lse);
     const at::Tensor ws = workspace_of(
         q, a[10], f_paged_ws(B, static_cast<int>(R), static_cast<int>(mb), static_cast<int>(H)));
-    return results(f_paged(as<uint16_t>(q), q.stride(0), q.stride(1), ptr(p.kv), as<float>(p.s), as<uint16_t>(p.pe),
+    return results(f_paged(as<uint16_t>(q), row_stride(q, 0), row_stride(q, 1), ptr(p.kv), as<float>(p.s), as<uint16_t>(p.pe),
                            as<int32_t>(bt), as<int32_t>(sl), B, static_cast<int>(R), static_cast<int>(mb), p.pages,
                            static_cast<int>(p.page), static_cast<int>(H), kLatent, kRope, static_cast<float>(scale),
-                           as<uint16_t>(o.out), as<float>(o.lse), ptr(ws), ws.numel(), stream_of(a[12], q)),
+                           as<uint16_t>(o.out), as<float>(o.lse), ptr(ws), ws.numel(), on.stream),
                    o, want_lse);
   });
 }

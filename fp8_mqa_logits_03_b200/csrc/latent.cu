@@ -1446,7 +1446,9 @@ __global__ void __launch_bounds__(kSpreadThreads) latent_spread_kernel(const __g
   if (blockIdx.x == 0 && blockIdx.y == 0) collect_status(p);
   const int2 e = p.group_meta[blockIdx.x];
   const int x = e.x, np = e.y;
-  if (np < 2) return;
+  // (a CTA that gave up has not written the entries of the groups that it never
+  // reached: what is there instead must not be followed out of the workspace)
+  if (np < 2 || x < 0 || x + static_cast<int64_t>(np - 1) * p.ncg >= static_cast<int64_t>(p.parts) * p.ncg) return;
   const int cols = p.R * p.H, cg = blockIdx.x % p.ncg;
   const int n = min(kAttnCols, cols - cg * kAttnCols);
   const int quad = blockIdx.y >> 2, vb = blockIdx.y & 3;

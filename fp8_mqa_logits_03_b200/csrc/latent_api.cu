@@ -159,6 +159,12 @@ int fp8idx_latent_store(const uint16_t* c, int64_t c_stride, const uint16_t* k_p
   if (q_pe) {
     FP8IDX_TRY(check_strides("q_pe", q_pe, q_row_stride, q_head_stride));
     FP8IDX_TRY(check_strides("q_out", q_out, out_row_stride, out_head_stride));
+    // the written rows lie apart, whichever of the two strides is the larger
+    const bool row_outer = out_row_stride >= out_head_stride;
+    const int64_t inner = row_outer ? out_head_stride : out_row_stride, outer = row_outer ? out_row_stride : out_head_stride;
+    const int64_t ni = row_outer ? H : T, no = row_outer ? T : H;
+    if ((ni > 1 && inner < kRope) || (no > 1 && outer < static_cast<__int128>(ni - 1) * inner + kRope))
+      return fail(FP8IDX_EINVAL, "the rows of q_out overlap");
   }
   if (!aligned(cos_sin, 16) || !aligned(positions, 8) || !aligned(slot, 8))
     return fail(FP8IDX_EINVAL, "cos_sin must be 16-byte aligned, positions and slot 8-byte aligned");

@@ -282,7 +282,7 @@ int fp8idx_topk_transform(const int32_t* idx, int64_t rows, int topk, const int3
  *   q_pe, q_out  [T, H, 64] bf16 with row and head strides in values, H in
  *              [1, 128]; q_out may be q_pe itself, and otherwise must not
  *              overlap it (it is usually the last 64 of the [T, H, 576]
- *              absorbed queries)
+ *              absorbed queries); its rows must not overlap one another
  * Every bf16 pointer and stride must be a multiple of 16 bytes.  Slots that
  * no token names are left untouched; two tokens naming one slot race.
  * No workspace.
@@ -314,8 +314,10 @@ int fp8idx_latent_store(const uint16_t* c, int64_t c_stride, const uint16_t* k_p
  *   slots      [rows, topk] int32, row stride ld_slots
  *   out        [rows, H, 512] bf16          lse  [rows, H] fp32 or NULL
  *   scale      positive and finite
- * ws / ws_bytes: as for fp8idx_mqa_logits_topk, of at least
- * fp8idx_sparse_latent_attention_workspace(rows, H, topk) bytes.
+ * out and lse overlap no input.  ws / ws_bytes: as for
+ * fp8idx_mqa_logits_topk, of at least
+ * fp8idx_sparse_latent_attention_workspace(rows, H, topk) bytes; what it
+ * holds before the call does not matter.
  */
 size_t fp8idx_sparse_latent_attention_workspace(int64_t rows, int H, int topk);
 int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,

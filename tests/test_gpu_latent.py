@@ -616,6 +616,86 @@ def test_wait_timeout_sets_status_and_recovers(fp8):
         _check_row(_np(out)[i], _np(lse)[i], qn[i], keys[sln[i]], fp8, f"row {i}")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_wait_timeout_with_groups_not_reached(fp8):
+    """The same where a CTA had further requests to come: what the workspace
+    held for them before is not followed."""
+    B, R, H, L = 5, 8, 128, 6000
+    table = torch.arange(94, dtype=torch.int32).repeat(B, 1).cuda()
+    dev, keys = _pool(94, fp8, 460)
+    q, qn = _q(B * R, H, 461)
+    lens = torch.full((B,), L, dtype=torch.int32).cuda()
+    ws = fx.alloc_workspace(fx.paged_latent_workspace_size(B, R, 94, H))
+    run = lambda **kw: fx.paged_latent_attention(q, block_table=table, seq_lens=lens, R=R, scale=SCALE, **dev, workspace=ws, **kw)  # noqa: E731
+    for fill in (0x7F, 0xFF, 0x01):
+        ws.fill_(fill)
+        torch.cuda.synchronize()
+        try:
+            fx.set_wait_limit_ns(2_000_000)
+            fx.debug_withhold_first_tile(True)
+            run()
+            st = fx.read_device_status(ws)
+        finally:
+            fx.debug_withhold_first_tile(False)
+            fx.set_wait_limit_ns(2_000_000_000)
+        assert st & fx.STATUS_WAIT_TIMEOUT, f"status {st:#x}"
+    out, lse = run(return_lse=True)
+    assert fx.read_device_status(ws) == 0
+    for i in (0, 39):
+        _check_row(_np(out)[i], _np(lse)[i], qn[i], keys[:L - R + i % R + 1], fp8, f"row {i}")
+
+
+def test_workspace_of_a_call_on_another_stream():
+    """The call makes its own workspace; what the current stream allocates and
+    writes meanwhile must not land in it."""
+    dev, keys = _pool(40, True, 470)
+    q, _ = _q(64, 64, 471)
+    sl = torch.from_numpy(_slots(64, 2048, 2560, 472)).cuda()
+    want = fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    n = fx.sparse_latent_workspace_size(64, 64, 2048)
+    got = []
+    for _ in range(20):
+        got.append(fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev, stream=s))
+        torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g, want)
+
+
+def test_strides_of_size_one_and_overlap():
+    """A dimension of size 1 may have any stride; output rows that overlap are refused."""
+    dev, keys = _pool(2, False, 480)
+    base = torch.randn(3, 577, dtype=torch.float32).to(BF).cuda()
+    q = base[:1, :576].unsqueeze(1)
+    sl = torch.arange(100, dtype=torch.int32)[None].cuda()
+    out, lse = fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev, return_lse=True)
+    _check_row(_np(out)[0], _np(lse)[0], _np(q)[0], keys[:100], False, "row 0")
+    x, qx, tab, pos, slot = _store_case(4, 2, False, True, 481, 2)
+    one = torch.zeros(4, 1, 64, dtype=BF).cuda().expand(4, 2, 64)
+    with pytest.raises(fx.Fp8IdxError):
+        fx.latent_store(x.cuda()[:, :512], x.cuda()[:, 512:], pos.cuda(), tab.cuda(), slot.cuda(), **dev,
+                        q_pe=qx.cuda()[..., :64], q_out=one)
+
+
+def test_no_backward():
+    """No gradient is dropped in silence: inputs that require one are refused, unless gradients are off."""
+    dev, _ = _pool(2, False, 490)
+    q, _ = _q(2, 4, 491)
+    sl = torch.arange(20, dtype=torch.int32).repeat(2, 1).cuda()
+    want = fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev)
+    q.requires_grad_()
+    with pytest.raises(ValueError, match="no backward"):
+        fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev)
+    with pytest.raises(ValueError, match="no backward"):
+        fx.paged_latent_attention(q, block_table=torch.zeros(2, 1, dtype=torch.int32).cuda(),
+                                  seq_lens=torch.ones(2, dtype=torch.int32).cuda(), R=1, scale=SCALE, **dev)
+    with torch.no_grad():
+        assert torch.equal(fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev), want)
+    assert torch.equal(fx.sparse_latent_attention(q.detach(), slots=sl, scale=SCALE, **dev), want)
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("fp8", [False, True])

@@ -47,6 +47,13 @@ def test_store_rejects(L):
     assert L.fp8idx_last_error() == b""
 
 
+@pytest.mark.parametrize("T,H,strides", [(4, 1, (0, 64)), (4, 1, (56, 64)), (1, 4, (64, 56)), (1, 4, (64, 0)), (4, 4, (64, 64)),
+                                         (4, 4, (248, 64)), (10, 4, (120, 1136)), (4, 3, (200, 72))])
+def test_store_rejects_overlapping_output_rows(L, T, H, strides):
+    assert _store(L, q=FAKE, o=FAKE, T=T, H=H, os_=strides) == fx.EINVAL
+    assert b"overlap" in L.fp8idx_last_error()
+
+
 def _sparse(L, q=FAKE, qs=(576, 576), kv=FAKE, s=None, pe=None, n=64, slots=FAKE, ld=16, rows=2, topk=16, H=4,
             latent=512, rope=64, scale=0.1, out=FAKE, lse=None, ws=FAKE, nb=1 << 30):
     return L.fp8idx_sparse_latent_attention(q, *qs, kv, s, pe, n, slots, ld, rows, topk, H, latent, rope, scale, out,
