@@ -70,10 +70,10 @@ struct Shape {
   static constexpr int kSoftmax = 128 * kSwg;
   static constexpr int kProducers = 128;
   static constexpr int kThreads = kSoftmax + kProducers + 64;
-  static constexpr int kFull = FP8 ? 3 : 2;       // announcements of a tile's parts
-  // the parts that announcement f covers (fp8: the second half's first)
-  __host__ __device__ static constexpr int first_part(int f) { return FP8 ? (f == 0 ? 2 : f == 1 ? 0 : f == 2 ? 4 : 5) : (f == 0 ? 0 : f == 1 ? 2 : 5); }
-  __host__ __device__ static constexpr int end_part(int f) { return FP8 ? (f == 0 ? 4 : f == 1 ? 2 : 5) : (f == 0 ? 2 : 5); }
+  static constexpr int kFull = FP8 ? 5 : 2;       // announcements of a tile's parts
+  // the parts that announcement f covers (fp8: 2, 3, 0, 1, 4, as they are converted)
+  __host__ __device__ static constexpr int first_part(int f) { return FP8 ? (f < 4 ? (f + 2) & 3 : f) : (f == 0 ? 0 : f == 1 ? 2 : 5); }
+  __host__ __device__ static constexpr int end_part(int f) { return FP8 ? first_part(f) + 1 : (f == 0 ? 2 : 5); }
 };
 constexpr int kMaxThreads = 448;
 static_assert(Shape<true>::kThreads <= kMaxThreads && Shape<false>::kThreads <= kMaxThreads, "threads");
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     for (int s = 0; s < kStages; ++s)
       for (int i = 0; i < kParts; ++i) {
         // codes: one arrival a warp; asynchronous copies: one a thread (bf16: and one with the tile's description)
-        mbar_init(&ms.full[s][i], FP8 && i < 2 ? kProducers / 32 : kProducers + (!FP8 && i == 0 ? 1 : 0));
+        mbar_init(&ms.full[s][i], FP8 && i < 4 ? kProducers / 32 : kProducers + (!FP8 && i == 0 ? 1 : 0));
         mbar_init(&ms.empty[s][i], 1);
       }
     mbar_init(&ms.q_full, kProducers);
@@ -742,21 +742,18 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const uint32_t dst = row_dst + st * kStageBytes;
       if (FP8 && !null) {
         // The codes land in the first half of the stage, and the rotated part,
-        // bf16 as it is, in its place.  The second half's codes become fp16 in
-        // the second half; then the others, two rows at a time into registers
-        // and from there, as fp16, into the first.
+        // bf16 as it is, in its place: parts 2 and 3 in part 0's, 0 and 1 in
+        // part 1's.  They become fp16 in this order, each as it lands, in its own
+        // place, which for the last two is where the ones before have landed.  A
+        // row's eight pieces are one warp's, landing and converted.
         const uint32_t land = dst + swz;
         if (pt < kAttnKeys) cp_async4(smem_u32(&ms.scale[st][0][pt]), p.s + max(key_slot, 0), key_slot >= 0 ? 4 : 0);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {  // the second half's codes into part 0, the first half's into part 1
-          if (c == 1 && !warp_wait(&ms.empty[st][1], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
+        for (int u = 0; u < 4; ++u) {  // part (u + 2) % 4 into chunk u
+          if (u == 2 && !warp_wait(&ms.empty[st][1], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
 #pragma unroll
-          for (int k = 0; k < NK; ++k) {
-            const uint8_t* at = row_at(row[k]) + (c == 0 ? 256 : 0);
-            const uint32_t n = row[k] >= 0 ? 16 : 0;
-            cp_async16(land + 2 * c * kChunkBytes + k * (kRows * 128), at, n);
-            cp_async16(land + (2 * c + 1) * kChunkBytes + k * (kRows * 128), at + 128, n);
-          }
+          for (int k = 0; k < NK; ++k)
+            cp_async16(land + u * kChunkBytes + k * (kRows * 128), row_at(row[k]) + ((u + 2) & 3) * 128, row[k] >= 0 ? 16 : 0);
           cp_async_commit();
         }
         if (!ok) break;
@@ -768,46 +765,38 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         for (int k = 0; k < NK; ++k)
           cp_async16(land + 8 * kChunkBytes + k * (kRows * 128),
                      p.pe + static_cast<int64_t>(max(row[k], 0)) * (kRope * 2) + piece * 16, row[k] >= 0 ? 16 : 0);
-        cp_async_arrive(&ms.full[st][2]);
+        cp_async_arrive(&ms.full[st][4]);
         cp_async_commit();
-        cp_async_wait<2>();
-        if (pt < kAttnKeys) {
-          // a scale of 0 (or below 2^-60, or of a key that does not exist)
-          // counts as 2^-60: its log and inverse are used
-          const float x = ms.scale[st][0][pt], y = x < 8.673617379884035e-19f ? 8.673617379884035e-19f : x;
-          ms.scale[st][0][pt] = y;
-          ms.scale[st][1][pt] = log2f(y);
-          ms.scale[st][2][pt] = 1.f / y;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (u == 0) cp_async_wait<4>();
+          else if (u == 1) cp_async_wait<3>();
+          else if (u == 2) cp_async_wait<2>();
+          else cp_async_wait<1>();
+          if (u == 0 && pt < kAttnKeys) {
+            // a scale of 0 (or below 2^-60, or of a key that does not exist)
+            // counts as 2^-60: its log and inverse are used
+            const float x = ms.scale[st][0][pt], y = x < 8.673617379884035e-19f ? 8.673617379884035e-19f : x;
+            ms.scale[st][0][pt] = y;
+            ms.scale[st][1][pt] = log2f(y);
+            ms.scale[st][2][pt] = 1.f / y;
+          }
+          uint4 raw[NK];
+#pragma unroll
+          for (int k = 0; k < NK; ++k) raw[k] = ld_shared16(land + u * kChunkBytes + k * (kRows * 128));
+          if (u == 3) __syncwarp();  // (this part's own place)
+#pragma unroll
+          for (int k = 0; k < NK; ++k) store_codes(raw[k], (u + 2) & 3, k, dst);
+          __syncwarp();
+          if (lane == 0 && !(withhold && u == 0)) mbar_arrive(&ms.full[st][u]);
         }
-#pragma unroll
-        for (int c = 2; c < 4; ++c)
-#pragma unroll
-          for (int k = 0; k < NK; ++k)
-            store_codes(ld_shared16(land + (c - 2) * kChunkBytes + k * (kRows * 128)), c, k, dst);
-        __syncwarp();
-        if (lane == 0 && !withhold) mbar_arrive(&ms.full[st][0]);
-        cp_async_wait<1>();
-#pragma unroll
-        for (int k = 0; k < NK; k += 2) {
-          uint4 raw[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            raw[u] = ld_shared16(land + (2 + (u & 1)) * kChunkBytes + (k + (u >> 1)) * (kRows * 128));
-          __syncwarp();  // (a row's eight pieces are one warp's, landing and converted)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) store_codes(raw[u], u & 1, k + (u >> 1), dst);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.full[st][1]);
       } else if (FP8) {
         // nothing to bring: every thread arrives for the rotated part, a warp for the others
         for (int f = 0; f < Sh::kFull; ++f) {
           if (f > 0 && (flags & kEnd)) break;
-          if (f > 0 && !warp_wait(&ms.empty[st][f == 1 ? 1 : 4], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
-          if (f == 2 && (!warp_wait(&ms.empty[st][2], ph ^ 1, abort_flag, &ms.status, limit) ||
-                         !warp_wait(&ms.empty[st][3], ph ^ 1, abort_flag, &ms.status, limit))) { ok = false; break; }
+          if (!(flags & kEnd) && !warp_wait(&ms.empty[st][Sh::first_part(f)], ph ^ 1, abort_flag, &ms.status, limit)) { ok = false; break; }
           __syncwarp();
-          if (f == 2 || lane == 0) mbar_arrive(&ms.full[st][f]);
+          if (f == 4 || lane == 0) mbar_arrive(&ms.full[st][f]);
         }
       } else {
 #pragma unroll
