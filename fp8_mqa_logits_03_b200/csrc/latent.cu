@@ -714,18 +714,19 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const uint32_t ph = (i >> 1) & 1;
       const int flags = d.flags;
       const bool null = flags & (kNull | kEnd);
-      if ((flags & kFirst) && !null && i > 0) {
-        // ---- the group's query columns; their place is free once the scores of tile i - 1 are done
-        // (and of tile i - 2: a tile i - 1 without keys has none)
-        if (!warp_wait(&ms.s_full[st ^ 1], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) break;
-        if (i > 1 && !warp_wait(&ms.s_full[st], ph ^ 1, abort_flag, &ms.status, limit)) break;
+      // The group's query columns; their place is free once the scores of tile
+      // i - 1 are done (and of tile i - 2: a tile i - 1 without keys has none).
+      const bool first = (flags & kFirst) && !null;
+      auto next_q = [&]() {
+        if (!warp_wait(&ms.s_full[st ^ 1], ((i - 1) >> 1) & 1, abort_flag, &ms.status, limit)) return false;
+        if (i > 1 && !warp_wait(&ms.s_full[st], ph ^ 1, abort_flag, &ms.status, limit)) return false;
         copy_q(d.group);
-      }
+        return true;
+      };
       if (i == 0 && null) cp_async_wait_all();  // the queries copied ahead are not used: out of the way of the next ones
-      float qfac[NK];
-      if ((flags & kFirst) && !null) {
-        if (FP8) convert_q(qfac);
-        else cp_async_arrive(&ms.q_full);
+      if (!FP8 && first) {
+        if (i > 0 && !next_q()) break;
+        cp_async_arrive(&ms.q_full);
       }
       // ---- describe the tile.  The entry was tile i - 4's; the values of
       // tile i - 2 have begun, so every role is past tile i - 4.
@@ -733,10 +734,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       if (pt == 0) {
         ms.info[i & (kInfo - 1)] = d;
         if (!FP8) mbar_arrive(&ms.full[st][0]);
-      }
-      if (FP8 && (flags & kFirst) && !null && piece == 0) {
-#pragma unroll
-        for (int k = 0; k < NK; ++k) ms.q_scale[st][r0 + kRows * k] = qfac[k];
       }
       const bool withhold = p.debug_withhold_first_tile && i == 0;
       const uint32_t dst = row_dst + st * kStageBytes;
@@ -767,6 +764,15 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
                      p.pe + static_cast<int64_t>(max(row[k], 0)) * (kRope * 2) + piece * 16, row[k] >= 0 ? 16 : 0);
         cp_async_arrive(&ms.full[st][4]);
         cp_async_commit();
+        if (first) {  // the queries, while the codes are on their way
+          if (i > 0 && !next_q()) break;
+          float qfac[NK];
+          convert_q(qfac);
+          if (piece == 0) {
+#pragma unroll
+            for (int k = 0; k < NK; ++k) ms.q_scale[st][r0 + kRows * k] = qfac[k];
+          }
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           if (u == 0) cp_async_wait<4>();
