@@ -42,7 +42,7 @@
 // cycles), its keys are written once, 72 KB: 2500 cycles.  4096 rows x 64
 // heads x 2048 bf16 keys take 1.46 ms (800 TFLOP/s), 2980 cycles a tile with
 // the segments' starts and ends; fp8 codes are written, read and written again
-// (another 64 KB) and take about 4000 (1024 rows x 128 heads: 0.98 ms).  Stages of 64 keys are the largest of which two fit beside
+// (another 64 KB) and take about 3800 (1024 rows x 128 heads: 0.94 ms).  Stages of 64 keys are the largest of which two fit beside
 // the queries; over one tile or two, waits for memory and hand-overs count:
 // one row of 16 heads x 2048 keys, a tile a CTA, takes 10.7 us.  Long
 // contexts with 64 columns a request reach 5.4 TB/s of keys.

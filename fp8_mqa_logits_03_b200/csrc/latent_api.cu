@@ -36,15 +36,19 @@ struct AttnPlan {
   size_t off_meta = 0, off_group = 0, off_ml = 0, off_o = 0, total = 0;
 };
 
-// What joining cut groups costs, in tiles of a CTA's time.
-constexpr int64_t kJoinTiles = 4;
+// What joining cut groups costs, in tiles of a CTA's time: more where a piece
+// has many columns and a group that is cut lies on CTAs that hold others' pieces
+// too.  (64 columns, 2048 slots, 120 rows: 66.5 us cut, 62.7 whole, six tiles
+// longer; 512 slots, 160 rows: 37.4 and 38.2, fp8 41.1 and 45.4, seven longer;
+// 16 columns, 120 rows: 56.9 and 58.3.)
+constexpr int64_t kJoinTiles = 4, kJoinTilesWide = 6;
 
 // One CTA per SM, split into column blocks of 64 (a block of every range runs
 // at the same time as the others of that range, so that they share its keys
 // in L2) and as many ranges of the tile axis as fit; a range holds at least
 // one tile.  Where all groups have the same number of tiles (`uniform`), the
-// ranges end with groups if that makes the longest one at most kJoinTiles
-// longer: nothing is then left to be joined; or else, under the same
+// ranges end with groups if that makes the longest one at most kJoinTiles (or
+// kJoinTilesWide) longer: nothing is then left to be joined; or else, under the same
 // condition, every group gets ranges of its own.
 AttnPlan plan_attn(int64_t groups, int64_t cols, int64_t tiles_per_group, bool uniform, int sms) {
   AttnPlan pl;
@@ -60,7 +64,7 @@ AttnPlan plan_attn(int64_t groups, int64_t cols, int64_t tiles_per_group, bool u
   if (uniform && groups > 0) {
     const int64_t even = ceil_div(tiles, pl.parts), most = std::min<int64_t>(pl.parts, groups);
     const int64_t each = ceil_div(groups, most), split = std::max<int64_t>(1, pl.parts / groups);
-    if (each * nt <= even + kJoinTiles) {
+    if (each * nt <= even + (cols > 32 && split == 1 ? kJoinTilesWide : kJoinTiles)) {
       pl.whole_groups = true;
       pl.parts = static_cast<int>(ceil_div(groups, each));
     } else if (groups <= pl.parts && ceil_div(nt, split) <= even + kJoinTiles) {
