@@ -268,6 +268,13 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                : "memory");
 }
 
+// The same, stored as they are.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -942,7 +949,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     // exchanged between the two warpgroups in the weights' buffer, while no weights are in it
     float* half_max = reinterpret_cast<float*>(smem + kOffP);
     float* stat_l1 = half_max;
-    uint8_t* prow = smem + kOffK + 8 * kChunkBytes + rr * 128 + 4 * (lane & 3);
+    const uint32_t prow = smem_u32(smem + kOffK + 8 * kChunkBytes) + (quad * 16 + (lane & 15)) * 128;  // weights: this lane's row to store
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float to_log2[2] = {p.scale_log2, p.scale_log2};
     bool dead = false;
@@ -1075,13 +1082,11 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           }
         }
       };
-      auto put_weights = [&]() {
+      auto put_weights = [&]() {  // two 8-key blocks of the warp's 16 columns at a time
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          uint8_t* at = prow + b * kStageBytes + (((wg * NJ + j) ^ (rr & 7)) << 4);
-          *reinterpret_cast<uint32_t*>(at) = w[2 * j];
-          *reinterpret_cast<uint32_t*>(at + 8 * 128) = w[2 * j + 1];
-        }
+        for (int j = 0; j < NJ; j += 2)
+          stmatrix_x4(prow + b * kStageBytes + (((wg * NJ + j + (lane >> 4)) ^ (lane & 7)) << 4), w[2 * j], w[2 * j + 1],
+                      w[2 * j + 2], w[2 * j + 3]);
       };
       const bool live = !(flags & (kNull | kEnd));
       // Pass 0: the weights with the maxima as they are (not on a segment's
