@@ -83,7 +83,7 @@ constexpr int kOffQ = 0;
 constexpr int kOffK = kStageBytes;              // the 64 query columns take as much as a stage
 constexpr int kOffP = kOffK + kStages * kStageBytes;
 constexpr int kOffMisc = kOffP + kChunkBytes;
-constexpr int kMiscBytes = 3072;
+constexpr int kMiscBytes = 3 * 1024;
 constexpr int kSmemBytes = kOffMisc + kMiscBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
