@@ -81,8 +81,8 @@ static_assert(Shape<true>::kThreads <= kMaxThreads && Shape<false>::kThreads <= 
 // shared memory, from a 1024-byte boundary
 constexpr int kOffQ = 0;
 constexpr int kOffK = kStageBytes;              // the 64 query columns take as much as a stage
-constexpr int kOffP = kOffK + kStages * kStageBytes;
-constexpr int kOffMisc = kOffP + kChunkBytes;
+constexpr int kOffX = kOffK + kStages * kStageBytes;  // softmax warps: maxima and sums exchanged, output transposed
+constexpr int kOffMisc = kOffX + kChunkBytes;
 constexpr int kMiscBytes = 3 * 1024;
 constexpr int kSmemBytes = kOffMisc + kMiscBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -946,8 +946,8 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
     // fp8: weights are fp16, whose range the maximum is moved away from the
     // lower end of (2^7 next to it, 2^15 before a rescale; 2^-24 is the smallest)
     constexpr float kBias = FP8 ? 7.f : 0.f;
-    // exchanged between the two warpgroups in the weights' buffer, while no weights are in it
-    float* half_max = reinterpret_cast<float*>(smem + kOffP);
+    // exchanged between the two warpgroups
+    float* half_max = reinterpret_cast<float*>(smem + kOffX);
     float* stat_l1 = half_max;
     const uint32_t prow = smem_u32(smem + kOffK + 8 * kChunkBytes) + (quad * 16 + (lane & 15)) * 128;  // weights: this lane's row to store
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -1107,16 +1107,14 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
           }
-          if (kSwg > 1) {
-            if ((lane & 3) == 0) {
-              half_max[wg * kAttnCols + rr] = mx[0];
-              half_max[wg * kAttnCols + rr + 8] = mx[1];
-            }
-            named_bar_sync(2, kSoftmax);
+          if ((lane & 3) == 0) {
+            half_max[wg * kAttnCols + rr] = mx[0];
+            half_max[wg * kAttnCols + rr + 8] = mx[1];
           }
+          named_bar_sync(2, kSoftmax);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (kSwg > 1) mx[h] = fmaxf(mx[h], half_max[(wg ^ 1) * kAttnCols + rr + 8 * h]);
+            mx[h] = fmaxf(mx[h], half_max[(wg ^ 1) * kAttnCols + rr + 8 * h]);
             float fac = 1.f;
             if (flags & kFirst) {
               m[h] = mx[h];
@@ -1194,7 +1192,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       const int n = min(kAttnCols, cols - cg * kAttnCols);
       const int64_t col0 = static_cast<int64_t>(group) * cols + cg * kAttnCols;
       if (tid < kAttnCols) {
-        const float mm = ms.stat_m[tid], ll = kSwg > 1 ? ms.stat_l[tid] + stat_l1[tid] : ms.stat_l[tid];
+        const float mm = ms.stat_m[tid], ll = ms.stat_l[tid] + stat_l1[tid];
         if (tid < n) {
           if (!direct) p.part_ml[static_cast<int64_t>(slot) * kAttnCols + tid] = make_float2(mm, ll);
           else if (p.lse) p.lse[col0 + tid] = (mm + log2f(ll)) * 0.69314718055994531f;
@@ -1204,10 +1202,10 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       named_bar_sync(2, kSoftmax);
       if (direct) {
         // This warpgroup's 32 columns: 32 values x 16 columns at a time,
-        // divided, rounded, transposed through the warp's part of the weights'
+        // divided, rounded, transposed through the warp's part of the exchange
         // buffer, and written as 64 bytes a column by four lanes.
         const int cb = wg * 32;
-        uint8_t* tb = smem + kOffP + warp * 1024;  // [16 columns][32 values], pieces swizzled
+        uint8_t* tb = smem + kOffX + warp * 1024;  // [16 columns][32 values], pieces swizzled
         const int mcol = (lane & 7) + (lane >> 4) * 8, mhalf = (lane >> 3) & 1;  // stmatrix: this lane's column, value half
         uint16_t* oo = p.out + (col0 + cb) * kLatent + quad * 32;
         if (cb < n) {
