@@ -123,6 +123,7 @@ struct Misc {
   float scale[2][3][kAttnKeys];  // fp8: the tile's key scales s, log2 s and 1 / s, by tile parity
   float q_scale[2][kAttnCols];   // fp8: what a column's scores are multiplied by (log2 units)
   float stat_m[kAttnCols], stat_l[kAttnCols];
+  uint32_t unfit[8];  // paged: by softmax warp, keys among 32 whose values it found not finite
   uint32_t tmem;
   int abort_flag;
   int status;       // device status bits of this CTA
@@ -972,7 +973,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
       }
       uint32_t w[2 * NJ], r[NR];
       float mx[2] = {-INFINITY, -INFINITY}, la[2];
-      bool poison = false;  // fp8: a key that a row must not see has a scale that is not finite
+      bool suspect = false;  // paged: the score of a key that its row must not see is not finite
       // The tile's scores (fp8: in log2 units, with the keys' scales), unseen ones -inf, and this thread's maxima.
       auto read_scores = [&]() {
         tmem_ld_16(tbase + kTmemS + b * 64 + wg * kKeys + lane_base, r);
@@ -1019,16 +1020,8 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           for (int j = 0; j < NR; ++j) {
             const int h = (j >> 1) & 1, bit = 8 * (j >> 2) + (j & 1);
             const bool real = (here >> bit) & 1, seen = (sees[h] >> bit) & 1;
-            if (PAGED && real && !seen && !(fabsf(__uint_as_float(r[j])) < INFINITY)) {
-              // a key that this row must not see is not finite: 0 * value would
-              // not be 0, so its values become 0 (rows that see it have a
-              // score that is not finite, and keep it)
-              uint8_t* krow = smem + kOffK + b * kStageBytes + (bit + cq) * 128;
-              for (int c = 0; c < 8; ++c)
-                for (int x = 0; x < 8; ++x)
-                  *reinterpret_cast<uint4*>(krow + c * kChunkBytes + x * 16) = make_uint4(0, 0, 0, 0);
-              poison = true;
-            }
+            // the key, or the query: drop_unfit_keys tells
+            if (PAGED && real && !seen && !(fabsf(__uint_as_float(r[j])) < INFINITY)) suspect = true;
             if (!seen) r[j] = 0xFF800000u;
           }
         }
@@ -1039,6 +1032,40 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) mx[h] = (FP8 ? mx[h] : mx[h] * to_log2[h]) - kBias;
+      };
+      // Keys that not every row of the group sees, and whose values are not
+      // finite: 0 * value would not be 0 in the rows that must not see them, so
+      // their values become 0 (and an fp8 pool's 1 / scale, for the weights'
+      // sums).  The values themselves tell: a score that is not finite may be
+      // the query's doing, and its other rows see the key as it is.  A thread
+      // looks at a quarter of a key; all softmax warps are here.
+      auto drop_unfit_keys = [&]() {
+#pragma unroll 1
+        for (int u = 0; u < Sh::kFull; ++u)  // (the tile landed long ago: this thread's view of it)
+          if (!warp_wait(&ms.full[b][u], (i >> 1) & 1, abort_flag, &ms.status, limit)) dead = true;
+        const int key = (warp & 1) * 32 + lane;
+        uint8_t* krow = smem + kOffK + b * kStageBytes + (warp >> 1) * 2 * kChunkBytes + key * 128;
+        constexpr uint32_t kInf = FP8 ? 0x7C00u : 0x7F80u;  // exponent bits of fp16, bf16
+        bool unfit = FP8 && !(fabsf(ms.scale[b][0][key]) < INFINITY);
+#pragma unroll 1
+        for (int x = 0; x < 16; ++x) {
+          const uint4 v = *reinterpret_cast<const uint4*>(krow + (x >> 3) * kChunkBytes + (x & 7) * 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t y = (&v.x)[e];
+            unfit = unfit || (y & kInf) == kInf || ((y >> 16) & kInf) == kInf;
+          }
+        }
+        const uint32_t found = __ballot_sync(0xFFFFFFFFu, unfit && key >= f.ends);
+        if (lane == 0) ms.unfit[warp] = found;
+        named_bar_sync(2, kSoftmax);
+        const uint32_t all = ms.unfit[warp & 1] | ms.unfit[2 + (warp & 1)] | ms.unfit[4 + (warp & 1)] | ms.unfit[6 + (warp & 1)];
+        if ((all >> lane) & 1) {
+#pragma unroll 1
+          for (int x = 0; x < 16; ++x)
+            *reinterpret_cast<uint4*>(krow + (x >> 3) * kChunkBytes + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          if (FP8 && warp < 2) ms.scale[b][2][key] = 0.f;
+        }
       };
       // The weights of this thread's keys, with the reference maxima as they
       // are, and their sums (packed pairs of keys).
@@ -1071,16 +1098,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
           unpack_f32x2(la2[h], a, c);
           la[h] = a + c;
         }
-        if (FP8 && PAGED && poison) {  // 0 * (1 / scale) is not 0 there: the sums again, without such keys
-          la[0] = la[1] = 0.f;
-#pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            float a, c;
-            unpack_f32x2(neg2[(j >> 1) & 1], a, c);
-            a = ex2(__uint_as_float(r[j]) + a);
-            if (a != 0.f) la[(j >> 1) & 1] += a * ms.scale[b][2][8 * (j >> 2) + cq + (j & 1)];
-          }
-        }
       };
       auto put_weights = [&]() {  // two 8-key blocks of the warp's 16 columns at a time
 #pragma unroll
@@ -1111,7 +1128,11 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
             half_max[wg * kAttnCols + rr] = mx[0];
             half_max[wg * kAttnCols + rr + 8] = mx[1];
           }
-          named_bar_sync(2, kSoftmax);
+          if (!PAGED) {
+            named_bar_sync(2, kSoftmax);
+          } else if (bar_red_or(2, kSoftmax, suspect)) {
+            drop_unfit_keys();
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             mx[h] = fmaxf(mx[h], half_max[(wg ^ 1) * kAttnCols + rr + 8 * h]);
@@ -1146,7 +1167,7 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
         if (weighs) weigh();
         if (weighs) put_weights();
         if (pass == 1) break;
-        const bool grow = mx[0] > m[0] + kRescaleLog2 || mx[1] > m[1] + kRescaleLog2;
+        const bool grow = mx[0] > m[0] + kRescaleLog2 || mx[1] > m[1] + kRescaleLog2 || (PAGED && suspect);
         const bool vote = bar_red_or(1, kSoftmax, dead || end || grow);
         if (vote && bar_red_or(1, kSoftmax, dead || end)) {
           leave = true;

@@ -752,3 +752,33 @@ def test_a_decode_step(fp8):
         at = _logical(table.numpy(), i // R, L)[:L - R + i % R + 1]
         tol, ltol = lo.limits(_np(q)[i], keys[at], SCALE, fp8)
         assert (np.abs(_np(full)[i] - _np(out)[i]) <= 2 * tol).all() and (np.abs(_np(fl)[i] - _np(lse)[i]) <= 2 * ltol).all()
+
+
+# ------------------------------------------------------------------ what one row holds stays out of the others
+
+@pytest.mark.parametrize("H", [16, 40])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("head", [None, 3])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_paged_non_finite_query_stays_in_its_column(fp8, head, value, H):
+    """A value that is not finite in the query of a request's first row (all
+    heads, or one): that row does not see the last keys, the others do."""
+    lengths, R = [70, 130, 65, 3, 64, 2], 4
+    dev, keys, table, q, qn = _paged_case(lengths, R, H, fp8, 600 + H)
+    hit = np.zeros((len(lengths) * R, H), bool)
+    hit[::R, slice(None) if head is None else head] = True
+    q[torch.from_numpy(hit).cuda(), 5] = value
+    out, lse = fx.paged_latent_attention(q, block_table=torch.from_numpy(table).cuda(),
+                                         seq_lens=torch.tensor(lengths, dtype=torch.int32).cuda(), R=R, scale=SCALE, **dev,
+                                         return_lse=True)
+    out, lse = _np(out), _np(lse)
+    for b, l in enumerate(lengths):
+        at = _logical(table, b, l)
+        for t in range(R):
+            i = b * R + t
+            seen = keys[at[:max(0, l - R + t + 1)]]
+            ok = ~hit[i] if len(seen) else np.ones(H, bool)     # a row without keys gives 0 and -inf whatever its query holds
+            if ok.any():
+                _check_row(out[i][ok], lse[i][ok], qn[i][ok], seen, fp8, f"request {b} (length {l}) row {t}")
+            if np.isnan(value) and not ok.all():
+                assert np.isnan(out[i][~ok]).all() and np.isnan(lse[i][~ok]).all()
