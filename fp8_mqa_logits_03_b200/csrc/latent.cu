@@ -1066,6 +1066,15 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
             *reinterpret_cast<uint4*>(krow + (x >> 3) * kChunkBytes + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
           if (FP8 && warp < 2) ms.scale[b][2][key] = 0.f;
         }
+        // a row that sees such a key gets NaN, also where its score is -inf (its weight 0, times a value that is gone)
+        const uint32_t lo = ms.unfit[0] | ms.unfit[2] | ms.unfit[4] | ms.unfit[6];
+        const uint32_t hi = ms.unfit[1] | ms.unfit[3] | ms.unfit[5] | ms.unfit[7];
+        const unsigned long long here = pack_u32x2(lo, hi) >> cq;
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+          const int bit = 8 * (j >> 2) + (j & 1);
+          if (((here >> bit) & 1) && cq + bit < f.ends + trow[(j >> 1) & 1]) r[j] = 0x7FC00000u;
+        }
       };
       // The weights of this thread's keys, with the reference maxima as they
       // are, and their sums (packed pairs of keys).

@@ -333,7 +333,10 @@ int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int6
  * [0, seq_lens[b] - R + t + 1).  Values, formulas and pool as above; a page
  * entry outside [0, num_pages) sets BAD_PAGE and its keys are left out, a
  * length beyond max_blocks * 64 is clamped and sets SEQ_TOO_LONG.  What the
- * pool holds past a request's length never reaches the outputs, NaN included.
+ * pool holds past a request's length never reaches the outputs, NaN included;
+ * a key whose latent values are not finite reaches only the rows that see it,
+ * which give NaN in those values at least, and a query that is not finite only
+ * its own row and head.
  *   q  [B * R, H, 576] bf16 with strides    block_table  [B, max_blocks] int32
  *   seq_lens [B] int32                      out, lse     [B * R, H, ...] as above
  */

@@ -782,3 +782,27 @@ def test_paged_non_finite_query_stays_in_its_column(fp8, head, value, H):
                 _check_row(out[i][ok], lse[i][ok], qn[i][ok], seen, fp8, f"request {b} (length {l}) row {t}")
             if np.isnan(value) and not ok.all():
                 assert np.isnan(out[i][~ok]).all() and np.isnan(lse[i][~ok]).all()
+
+
+def test_paged_infinite_key_that_some_rows_see():
+    """A key with an infinite value that only a request's later rows see: it
+    stays out of the earlier ones, and shows in those that see it, where its
+    score is -inf (weight 0, and 0 times infinity) too."""
+    lengths, R, H = [70, 130, 64, 3], 4, 16
+    dev, keys, table, q, qn = _paged_case(lengths, R, H, False, 650)
+    for b, l in enumerate(lengths):
+        dev["kv_pages"].view(-1, 576)[int(_logical(table, b, l)[-2]), 7] = -float("inf")   # rows R - 2 and R - 1 see it
+    q[..., 7] = 1.0                                                                        # a score of -inf
+    qn = _np(q)
+    out, lse = fx.paged_latent_attention(q, block_table=torch.from_numpy(table).cuda(),
+                                         seq_lens=torch.tensor(lengths, dtype=torch.int32).cuda(), R=R, scale=SCALE, **dev,
+                                         return_lse=True)
+    out, lse = _np(out), _np(lse)
+    for b, l in enumerate(lengths):
+        at = _logical(table, b, l)
+        for t in range(R):
+            i = b * R + t
+            if t < R - 2:
+                _check_row(out[i], lse[i], qn[i], keys[at[:max(0, l - R + t + 1)]], False, f"request {b} row {t}")
+            else:
+                assert np.isnan(out[i][:, 7]).all(), f"request {b} row {t}"
