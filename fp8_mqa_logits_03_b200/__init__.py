@@ -404,6 +404,7 @@ def latent_store(c, k_pe, positions, cos_sin, slot_mapping, kv_pages, s_pages=No
 
 
 def sparse_latent_workspace_size(rows: int, heads: int, topk: int) -> int:
+    """Bytes of workspace that serve these sizes and all smaller ones (paged_latent_workspace_size too)."""
     return int(lib().fp8idx_sparse_latent_attention_workspace(rows, heads, topk))
 
 

@@ -36,6 +36,20 @@ struct AttnPlan {
   size_t off_meta = 0, off_group = 0, off_ml = 0, off_o = 0, total = 0;
 };
 
+// The workspace's parts, for a grid of `grid` CTAs.
+void lay_out(AttnPlan& pl, int64_t grid) {
+  int64_t off = kStatusBytes;
+  pl.off_meta = off;
+  off += round_up(grid * 16, 256);
+  pl.off_group = off;
+  off += round_up(kSpreadGroups * static_cast<int64_t>(pl.ncg) * 8, 256);
+  pl.off_ml = off;
+  off += round_up(grid * 2 * kAttnCols * 8, 256);
+  pl.off_o = off;
+  if (!pl.whole_groups) off += grid * 2 * kAttnCols * kLatent * 4;
+  pl.total = static_cast<size_t>(off);
+}
+
 // What joining cut groups costs, in tiles of a CTA's time: more where a piece
 // has many columns and a group that is cut lies on CTAs that hold others' pieces
 // too.  (64 columns, 2048 slots, 120 rows: 66.5 us cut, 62.7 whole, six tiles
@@ -71,18 +85,20 @@ AttnPlan plan_attn(int64_t groups, int64_t cols, int64_t tiles_per_group, bool u
       pl.parts = static_cast<int>(groups * split);  // a group's own ranges: none holds parts of two
     }
   }
-  const int64_t grid = static_cast<int64_t>(pl.parts) * pl.ncg;
-  int64_t off = kStatusBytes;
-  pl.off_meta = off;
-  off += round_up(grid * 16, 256);
-  pl.off_group = off;
-  off += round_up(kSpreadGroups * static_cast<int64_t>(pl.ncg) * 8, 256);
-  pl.off_ml = off;
-  off += round_up(grid * 2 * kAttnCols * 8, 256);
-  pl.off_o = off;
-  if (!pl.whole_groups) off += grid * 2 * kAttnCols * kLatent * 4;
-  pl.total = static_cast<size_t>(off);
+  lay_out(pl, static_cast<int64_t>(pl.parts) * pl.ncg);
   return pl;
+}
+
+// What the workspace queries give: enough for these sizes and for all smaller
+// ones, though fewer rows may take more (a plan without cut groups has no
+// partial sums, and the number of column blocks decides how many CTAs fit).
+// The grid is at most one CTA an SM, and a CTA for each tile and column block.
+size_t attn_workspace(int64_t groups, int64_t cols, int64_t tiles_per_group, int sms) {
+  AttnPlan pl;
+  pl.ncg = static_cast<int>(ceil_div(cols, kAttnCols));
+  const int64_t tiles = std::max<int64_t>(1, groups) * std::max<int64_t>(1, tiles_per_group);
+  lay_out(pl, std::min<int64_t>(std::max(sms, pl.ncg), tiles * pl.ncg));
+  return pl.total;
 }
 
 int check_latent_shape(int H, int latent, int rope) {
@@ -207,7 +223,7 @@ size_t fp8idx_sparse_latent_attention_workspace(int64_t rows, int H, int topk) {
   if (rows < 0 || H < 1 || H > kAttnMaxHeads || topk < 0) return 0;
   const int sms = sms_cached();
   if (sms <= 0) return 0;
-  return plan_attn(rows, H, topk_tiles(topk), true, sms).total;
+  return attn_workspace(rows, H, topk_tiles(topk), sms);
 }
 
 int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -253,7 +269,7 @@ size_t fp8idx_paged_latent_attention_workspace(int64_t B, int R, int max_blocks,
   if (B < 0 || R < 1 || R > 8 || H < 1 || H > kAttnMaxHeads || max_blocks < 1) return 0;
   const int sms = sms_cached();
   if (sms <= 0) return 0;
-  return plan_attn(B, static_cast<int64_t>(R) * H, max_blocks, false, sms).total;
+  return attn_workspace(B, static_cast<int64_t>(R) * H, max_blocks, sms);
 }
 
 int fp8idx_paged_latent_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,

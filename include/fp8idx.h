@@ -317,7 +317,9 @@ int fp8idx_latent_store(const uint16_t* c, int64_t c_stride, const uint16_t* k_p
  * out and lse overlap no input.  ws / ws_bytes: as for
  * fp8idx_mqa_logits_topk, of at least
  * fp8idx_sparse_latent_attention_workspace(rows, H, topk) bytes; what it
- * holds before the call does not matter.
+ * holds before the call does not matter.  The size grows with each of its
+ * arguments (up to 39 MB on 148 SMs), here and for the paged form: a
+ * workspace for the largest batch serves every smaller one.
  */
 size_t fp8idx_sparse_latent_attention_workspace(int64_t rows, int H, int topk);
 int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride,

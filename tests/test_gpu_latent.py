@@ -806,3 +806,27 @@ def test_paged_infinite_key_that_some_rows_see():
                 _check_row(out[i], lse[i], qn[i], keys[at[:max(0, l - R + t + 1)]], False, f"request {b} row {t}")
             else:
                 assert np.isnan(out[i][:, 7]).all(), f"request {b} row {t}"
+
+
+def test_workspace_of_the_largest_sizes_serves_all_smaller_ones():
+    """A server reserves one workspace for its largest batch: no smaller one may ask for more."""
+    rows = [*range(1, 301), 512, 1000, 1024, 4096]
+    heads = (1, 16, 32, 33, 64, 65, 128)
+    topks = (0, 1, 64, 65, 128, 640, 2048)
+    sizes = np.array([[[fx.sparse_latent_workspace_size(r, h, k) for k in topks] for h in heads] for r in rows])
+    assert (sizes > 0).all()
+    for axis in range(3):
+        assert (np.diff(sizes, axis=axis) >= 0).all(), ("rows", "heads", "topk")[axis]
+    sizes = np.array([[[[fx.paged_latent_workspace_size(b, r, m, h) for h in heads] for m in (1, 2, 3, 5, 33, 2048)] for r in range(1, 9)]
+                      for b in (1, 2, 7, 32, 33, 100, 148, 149, 1000)])
+    assert (sizes > 0).all()
+    for axis in range(4):
+        assert (np.diff(sizes, axis=axis) >= 0).all(), ("requests", "rows a request", "blocks", "heads")[axis]
+    dev, _ = _pool(40, True, 660)
+    ws = fx.alloc_workspace(fx.sparse_latent_workspace_size(296, 64, 2048))
+    for n in (296, 160, 115, 116, 1):
+        q, _ = _q(n, 64, 661)
+        sl = torch.from_numpy(_slots(n, 2048, 2560, 662)).cuda()
+        want = fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev)
+        assert torch.equal(fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev, workspace=ws), want)
+        assert fx.read_device_status(ws) == 0
