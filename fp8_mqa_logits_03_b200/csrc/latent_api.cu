@@ -157,6 +157,16 @@ int run_attn(LatentAttnParams& p, const AttnPlan& pl, bool paged, bool fp8, void
 
 int64_t topk_tiles(int topk) { return ceil_div(topk, kAttnKeys); }
 
+// Sizes (not negative) whose products below, in int, int64 or bytes, cannot
+// overflow: the rows are bounded before anything is multiplied by them.
+bool sparse_sizes_fit(int64_t rows, int topk) {
+  return rows <= (int64_t(1) << 25) && topk <= (1 << 24) && rows * (topk_tiles(topk) + 1) < (int64_t(1) << 31);
+}
+bool paged_sizes_fit(int64_t B, int R, int max_blocks) {
+  return B <= (int64_t(1) << 25) / R && B * max_blocks < (int64_t(1) << 31) &&
+         static_cast<int64_t>(max_blocks) * kPageSize < (int64_t(1) << 31) - kAttnKeys;
+}
+
 }  // namespace
 
 extern "C" {
@@ -220,7 +230,7 @@ int fp8idx_latent_store(const uint16_t* c, int64_t c_stride, const uint16_t* k_p
 }
 
 size_t fp8idx_sparse_latent_attention_workspace(int64_t rows, int H, int topk) {
-  if (rows < 0 || H < 1 || H > kAttnMaxHeads || topk < 0) return 0;
+  if (rows < 0 || H < 1 || H > kAttnMaxHeads || topk < 0 || !sparse_sizes_fit(rows, topk)) return 0;
   const int sms = sms_cached();
   if (sms <= 0) return 0;
   return attn_workspace(rows, H, topk_tiles(topk), sms);
@@ -234,8 +244,7 @@ int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int6
   FP8IDX_TRY(check_latent_shape(H, latent, rope));
   FP8IDX_TRY(check_scale(scale));
   if (rows < 0 || topk < 0) return fail(FP8IDX_EINVAL, "negative size");
-  if (rows > (int64_t(1) << 25) || topk > (1 << 24) || rows * (topk_tiles(topk) + 1) >= (int64_t(1) << 31))
-    return fail(FP8IDX_EINVAL, "size too large");
+  if (!sparse_sizes_fit(rows, topk)) return fail(FP8IDX_EINVAL, "size too large");
   FP8IDX_TRY(check_pool(kv_pool, s_pool, pe_pool, num_slots));
   if (rows == 0) return ok();
   if (!q || !out || (topk > 0 && !slots)) return fail(FP8IDX_EINVAL, "null q, slots or out");
@@ -266,7 +275,7 @@ int fp8idx_sparse_latent_attention(const uint16_t* q, int64_t q_row_stride, int6
 }
 
 size_t fp8idx_paged_latent_attention_workspace(int64_t B, int R, int max_blocks, int H) {
-  if (B < 0 || R < 1 || R > 8 || H < 1 || H > kAttnMaxHeads || max_blocks < 1) return 0;
+  if (B < 0 || R < 1 || R > 8 || H < 1 || H > kAttnMaxHeads || max_blocks < 1 || !paged_sizes_fit(B, R, max_blocks)) return 0;
   const int sms = sms_cached();
   if (sms <= 0) return 0;
   return attn_workspace(B, static_cast<int64_t>(R) * H, max_blocks, sms);
@@ -283,9 +292,7 @@ int fp8idx_paged_latent_attention(const uint16_t* q, int64_t q_row_stride, int64
   if (R < 1 || R > 8) return fail(FP8IDX_EUNSUPPORTED, "rows per request must be in [1, 8] (got %d)", R);
   if (B < 0 || num_pages < 0 || max_blocks < 1) return fail(FP8IDX_EINVAL, "bad sizes");
   if (num_pages >= (int64_t(1) << 31) / kPageSize) return fail(FP8IDX_EINVAL, "pool too large");
-  if (B * R > (int64_t(1) << 25) || B * max_blocks >= (int64_t(1) << 31) ||
-      static_cast<int64_t>(max_blocks) * kPageSize >= (int64_t(1) << 31) - kAttnKeys)
-    return fail(FP8IDX_EINVAL, "size too large");
+  if (!paged_sizes_fit(B, R, max_blocks)) return fail(FP8IDX_EINVAL, "size too large");
   FP8IDX_TRY(check_pool(kv_pages, s_pages, pe_pages, num_pages * kPageSize));
   if (B == 0) return ok();
   if (!q || !out || !block_table || !seq_lens) return fail(FP8IDX_EINVAL, "null q, block_table, seq_lens or out");

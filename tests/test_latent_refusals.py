@@ -131,3 +131,18 @@ def test_binding_rejects_host_tensors():
     with pytest.raises(ValueError, match="both"):
         fx.latent_store(q[:, 0, :512], q[:, 0, 512:], torch.zeros(2, dtype=torch.int64), torch.zeros(4, 64),
                         torch.zeros(2, dtype=torch.int64), kv, s_pages=torch.zeros(1, 64))
+
+
+@pytest.mark.parametrize("B,R,mb", [(1 << 61, 8, 8), (1 << 62, 4, 4), (1 << 61, 8, 1 << 20), ((1 << 25) // 8 + 1, 8, 1), (1 << 62, 1, 1),
+                                    ((1 << 63) - 1, 8, (1 << 31) - 1)])
+def test_paged_rejects_sizes_whose_products_overflow(L, B, R, mb):
+    assert _paged(L, B=B, R=R, mb=mb) == fx.EINVAL
+    assert b"too large" in L.fp8idx_last_error()
+    assert L.fp8idx_paged_latent_attention_workspace(B, R, mb, 4) == 0
+
+
+@pytest.mark.parametrize("rows,topk", [(1 << 62, 16), ((1 << 63) - 1, (1 << 31) - 1), ((1 << 25) + 1, 1), (1, (1 << 24) + 1), (1 << 25, 1 << 16)])
+def test_sparse_rejects_sizes_whose_products_overflow(L, rows, topk):
+    assert _sparse(L, rows=rows, topk=topk, ld=topk) == fx.EINVAL
+    assert b"too large" in L.fp8idx_last_error()
+    assert L.fp8idx_sparse_latent_attention_workspace(rows, 4, topk) == 0
