@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -133,10 +134,20 @@ struct OnStream {
 // The stride of a dimension; one of size 1 has none that matters.
 int64_t row_stride(const at::Tensor& t, int64_t d) { return t.size(d) > 1 ? t.stride(d) : 0; }
 
-// The calls have no backward pass: a gradient must not be lost in silence.
+// The calls have no backward pass and carry no tangents: neither must be lost
+// in silence.  Every floating-point tensor of a call is looked at, those that
+// it writes among them.
 void no_grad(const at::Tensor& t, const char* name) {
-  if (t.defined() && t.requires_grad() && c10::GradMode::is_enabled())
+  if (!t.defined()) return;
+  if (t.requires_grad() && c10::GradMode::is_enabled())
     throw ValueError(std::string(name) + " requires grad, and this call has no backward: detach it or call under torch.no_grad()");
+  if (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+    throw ValueError(std::string(name) + " has a tangent, and this call has no forward-mode derivative: detach it");
+}
+void no_grad(const Pool& p) {
+  no_grad(p.kv, "kv_pages");
+  no_grad(p.s, "s_pages");
+  no_grad(p.pe, "pe_pages");
 }
 
 struct Outputs {
@@ -158,6 +169,8 @@ Outputs outputs(const at::Tensor& q, PyObject* out, PyObject* lse, bool want_lse
   }
   same_device(q, r.out, "out");
   same_device(q, r.lse, "lse");
+  no_grad(r.out, "out");
+  no_grad(r.lse, "lse");
   return r;
 }
 
@@ -240,7 +253,8 @@ PyObject* latent_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int interleaved = PyObject_IsTrue(a[10]);
     no_grad(c, "c");
     no_grad(k_pe, "k_pe");
-    no_grad(p.kv, "kv_pages");
+    no_grad(cs, "cos_sin");
+    no_grad(p);
     const OnStream on(a[11], p.kv);
     return PyLong_FromLong(f_store(as<uint16_t>(c), row_stride(c, 0), as<uint16_t>(k_pe), row_stride(k_pe, 0), T, as<int64_t>(pos),
                                    as<float>(cs), cs.size(0), interleaved, as<int64_t>(slot), p.pages * kPage,
@@ -266,7 +280,7 @@ PyObject* sparse_latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyErr_Occurred()) return nullptr;
     const bool want_lse = PyObject_IsTrue(a[9]);
     no_grad(q, "q");
-    no_grad(p.kv, "kv_pages");
+    no_grad(p);
     const OnStream on(a[10], q);
     const Outputs o = outputs(q, a[6], a[7], want_lse);
     const at::Tensor ws = workspace_of(q, a[8], f_sparse_ws(nr, static_cast<int>(H), static_cast<int>(topk)));
@@ -299,7 +313,7 @@ PyObject* paged_latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(q, sl, "seq_lens");
     const bool want_lse = PyObject_IsTrue(a[11]);
     no_grad(q, "q");
-    no_grad(p.kv, "kv_pages");
+    no_grad(p);
     const OnStream on(a[12], q);
     const Outputs o = outputs(q, a[8], a[9], want_lse);
     const at::Tensor ws = workspace_of(

@@ -830,3 +830,47 @@ def test_workspace_of_the_largest_sizes_serves_all_smaller_ones():
         want = fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev)
         assert torch.equal(fx.sparse_latent_attention(q, slots=sl, scale=SCALE, **dev, workspace=ws), want)
         assert fx.read_device_status(ws) == 0
+
+
+def test_no_gradient_is_lost_in_silence():
+    """Every floating-point tensor of the calls, given outputs among them, and
+    tangents of forward mode."""
+    import torch.autograd.forward_ad as fwad
+    dev, _ = _pool(2, True, 670)
+    q, _ = _q(2, 4, 671)
+    sl = torch.arange(20, dtype=torch.int32).repeat(2, 1).cuda()
+    table, lens = torch.zeros(2, 1, dtype=torch.int32).cuda(), torch.ones(2, dtype=torch.int32).cuda()
+    x, qx, tab, pos, slot = _store_case(4, 2, True, True, 672, 2)
+    x, qx, tab, pos, slot = x.cuda(), qx.cuda(), tab.cuda(), pos.cuda(), slot.cuda()
+    bufs = dict(out=torch.zeros(2, 4, 512, dtype=BF).cuda(), lse=torch.zeros(2, 4).cuda())
+
+    def sparse(**kw):
+        a = dict(q=q, slots=sl, scale=SCALE, **dev, **bufs)
+        fx.sparse_latent_attention(**{**a, **kw})
+
+    def paged(**kw):
+        a = dict(q=q, block_table=table, seq_lens=lens, R=1, scale=SCALE, **dev, **bufs)
+        fx.paged_latent_attention(**{**a, **kw})
+
+    def store(**kw):
+        a = dict(c=x[:, :512], k_pe=x[:, 512:], positions=pos, cos_sin=tab, slot_mapping=slot, **dev, q_pe=qx[..., :64],
+                 q_out=torch.zeros(4, 2, 64, dtype=BF).cuda())
+        fx.latent_store(**{**a, **kw})
+
+    given = {sparse: dict(q=q, s_pages=dev["s_pages"], pe_pages=dev["pe_pages"], **bufs),
+             paged: dict(q=q, s_pages=dev["s_pages"], pe_pages=dev["pe_pages"], **bufs),
+             store: dict(c=x[:, :512], k_pe=x[:, 512:], cos_sin=tab, s_pages=dev["s_pages"], pe_pages=dev["pe_pages"], q_pe=qx[..., :64],
+                         q_out=torch.zeros(4, 2, 64, dtype=BF).cuda())}
+    for call, tensors in given.items():
+        call()
+        for name, t in tensors.items():
+            leaf = t.detach().clone().requires_grad_()
+            with pytest.raises(ValueError, match=name + ".*no backward"):
+                call(**{name: leaf})
+            with torch.no_grad():
+                call(**{name: leaf})
+            with fwad.dual_level():
+                dual = fwad.make_dual(t.detach().clone(), torch.ones_like(t))
+                with pytest.raises(ValueError, match=name + ".*tangent"):
+                    call(**{name: dual})
+    torch.cuda.synchronize()
