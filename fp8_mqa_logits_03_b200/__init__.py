@@ -366,7 +366,8 @@ def _bind():
     global _bind_module
     if _bind_module is None:
         lib()
-        path = os.path.join(_HERE, "_bind.so")
+        from .build import bind_path
+        path = bind_path()   # of this interpreter and this torch
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with `python -m fp8_mqa_logits_03_b200.build`")
         loader = importlib.machinery.ExtensionFileLoader("_bind", path)

@@ -12,7 +12,6 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8idx.so")
 SOURCES = ["kernels.cu", "quant.cu", "index_prep.cu", "latent_store.cu", "latent.cu", "latent_api.cu", "api.cu"]
-BIND = os.path.join(HERE, "_bind.so")  # the compiled Python side of the latent calls
 DEPS = SOURCES + ["api_common.h", "kernels.cuh", "latent.cuh", "ptx.cuh", "select.cuh", "wait.cuh"]
 HEADER = os.path.join(os.path.dirname(HERE), "include", "fp8idx.h")
 # the headers each source includes (its object is rebuilt when one changes)
@@ -34,6 +33,13 @@ def nvcc_path() -> str:
     return cand
 
 
+def bind_path() -> str:
+    """The compiled Python side of the latent calls.  It holds at::Tensor's layout and this interpreter's
+    ABI, so its name carries both: another Python or torch neither loads it nor takes it as built."""
+    import torch
+    return os.path.join(HERE, f"_bind.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}.so")
+
+
 def _newer(target: str, deps) -> bool:
     """Whether `target` is missing or older than one of `deps`."""
     if not os.path.exists(target):
@@ -42,9 +48,12 @@ def _newer(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _bind_stale() -> bool:
+    return _newer(bind_path(), [os.path.join(CSRC, "bind.cpp"), HEADER, os.path.abspath(__file__)])
+
+
 def _stale() -> bool:
-    return (_newer(LIB, [os.path.join(CSRC, f) for f in DEPS] + [HEADER])
-            or _newer(BIND, [os.path.join(CSRC, "bind.cpp"), HEADER]))
+    return _newer(LIB, [os.path.join(CSRC, f) for f in DEPS] + [HEADER, os.path.abspath(__file__)]) or _bind_stale()
 
 
 def build_bind() -> None:
@@ -52,7 +61,8 @@ def build_bind() -> None:
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
-    tmp = BIND + f".tmp{os.getpid()}"
+    path = bind_path()
+    tmp = path + f".tmp{os.getpid()}"
     subprocess.check_call(
         [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared",
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -60,7 +70,7 @@ def build_bind() -> None:
          "-I" + sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "bind.cpp"),
          "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"],
         cwd=HERE)
-    os.replace(tmp, BIND)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -84,7 +94,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     with ThreadPoolExecutor(len(SOURCES) + 1) as pool:
         bind = None
-        if force or _newer(BIND, [os.path.join(CSRC, "bind.cpp"), HEADER]):
+        if force or _bind_stale():
             bind = pool.submit(build_bind)
         objs = list(pool.map(compile_one, SOURCES))
         if bind is not None:

@@ -146,3 +146,32 @@ def test_sparse_rejects_sizes_whose_products_overflow(L, rows, topk):
     assert _sparse(L, rows=rows, topk=topk, ld=topk) == fx.EINVAL
     assert b"too large" in L.fp8idx_last_error()
     assert L.fp8idx_sparse_latent_attention_workspace(rows, 4, topk) == 0
+
+
+def test_binding_belongs_to_one_interpreter_and_torch(L, monkeypatch):
+    """A binding that another torch or Python built is neither loaded nor taken as up to date."""
+    import sysconfig
+    assert not build._stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "1.0.0")
+        m.setattr(fx, "_bind_module", None)
+        assert build._stale()
+        with pytest.raises(RuntimeError, match="build it"):
+            fx._bind()
+    with monkeypatch.context() as m:
+        of = sysconfig.get_config_var
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-30-other" if name == "SOABI" else of(name))
+        m.setattr(fx, "_bind_module", None)
+        assert build._stale()
+        with pytest.raises(RuntimeError, match="build it"):
+            fx._bind()
+    assert not build._stale()
+
+
+def test_build_script_is_a_dependency(L, monkeypatch):
+    """Other compiler flags mean another library and another binding."""
+    import os
+    seen = []
+    monkeypatch.setattr(build, "_newer", lambda target, deps: seen.append([os.path.abspath(d) for d in deps]) or False)
+    build._stale()
+    assert len(seen) == 2 and all(os.path.abspath(build.__file__) in deps for deps in seen)
