@@ -325,6 +325,47 @@ __device__ __forceinline__ int group_len(const LatentAttnParams& p, int g) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kAttnKeys - 1) / kAttnKeys); }
 
+// Keys of a tile that not every row of the group sees (those from `ends` on),
+// and whose values are not finite: 0 * value would not be 0 in the rows that
+// must not see them, so their values become 0 (and an fp8 pool's 1 / scale, for
+// the weights' sums).  The values themselves tell: a score that is not finite
+// may be the query's doing, and its other rows see the key as it is.  All eight
+// softmax warps call this, a thread looks at a quarter of a key.  Returns the
+// first such key (128: none).  Out of line: it is rare.
+template <bool FP8>
+__device__ __noinline__ int drop_unfit_keys(Misc& ms, uint8_t* stage, int b, uint32_t parity, int ends, volatile int* abort_flag,
+                                             unsigned long long limit) {
+#pragma unroll 1
+  for (int u = 0; u < Shape<FP8>::kFull; ++u)  // the tile landed long ago; this is for the thread's own view of it
+    warp_wait(&ms.full[b][u], parity, abort_flag, &ms.status, limit);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, key = (warp & 1) * 32 + lane;
+  uint8_t* krow = stage + (warp >> 1) * 2 * kChunkBytes + key * 128;
+  constexpr uint32_t kInf = FP8 ? 0x7C00u : 0x7F80u;  // exponent bits of fp16, bf16
+  bool unfit = FP8 && !(fabsf(ms.scale[b][0][key]) < INFINITY);
+#pragma unroll 1
+  for (int x = 0; x < 16; ++x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(krow + (x >> 3) * kChunkBytes + (x & 7) * 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t y = (&v.x)[e];
+      unfit = unfit || (y & kInf) == kInf || ((y >> 16) & kInf) == kInf;
+    }
+  }
+  const uint32_t found = __ballot_sync(0xFFFFFFFFu, unfit && key >= ends);
+  if (lane == 0) ms.unfit[warp] = found;
+  named_bar_sync(2, Shape<FP8>::kSoftmax);
+  const uint32_t all = ms.unfit[warp & 1] | ms.unfit[2 + (warp & 1)] | ms.unfit[4 + (warp & 1)] | ms.unfit[6 + (warp & 1)];
+  if ((all >> lane) & 1) {
+#pragma unroll 1
+    for (int x = 0; x < 16; ++x)
+      *reinterpret_cast<uint4*>(krow + (x >> 3) * kChunkBytes + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+    if (FP8 && warp < 2) ms.scale[b][2][key] = 0.f;
+  }
+  const uint32_t lo = ms.unfit[0] | ms.unfit[2] | ms.unfit[4] | ms.unfit[6];
+  const uint32_t hi = ms.unfit[1] | ms.unfit[3] | ms.unfit[5] | ms.unfit[7];
+  return lo ? __ffs(lo) - 1 : hi ? 31 + __ffs(hi) : kAttnKeys + kPageSize;
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------- the kernel
@@ -1033,49 +1074,6 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
 #pragma unroll
         for (int h = 0; h < 2; ++h) mx[h] = (FP8 ? mx[h] : mx[h] * to_log2[h]) - kBias;
       };
-      // Keys that not every row of the group sees, and whose values are not
-      // finite: 0 * value would not be 0 in the rows that must not see them, so
-      // their values become 0 (and an fp8 pool's 1 / scale, for the weights'
-      // sums).  The values themselves tell: a score that is not finite may be
-      // the query's doing, and its other rows see the key as it is.  A thread
-      // looks at a quarter of a key; all softmax warps are here.
-      auto drop_unfit_keys = [&]() {
-#pragma unroll 1
-        for (int u = 0; u < Sh::kFull; ++u)  // (the tile landed long ago: this thread's view of it)
-          if (!warp_wait(&ms.full[b][u], (i >> 1) & 1, abort_flag, &ms.status, limit)) dead = true;
-        const int key = (warp & 1) * 32 + lane;
-        uint8_t* krow = smem + kOffK + b * kStageBytes + (warp >> 1) * 2 * kChunkBytes + key * 128;
-        constexpr uint32_t kInf = FP8 ? 0x7C00u : 0x7F80u;  // exponent bits of fp16, bf16
-        bool unfit = FP8 && !(fabsf(ms.scale[b][0][key]) < INFINITY);
-#pragma unroll 1
-        for (int x = 0; x < 16; ++x) {
-          const uint4 v = *reinterpret_cast<const uint4*>(krow + (x >> 3) * kChunkBytes + (x & 7) * 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t y = (&v.x)[e];
-            unfit = unfit || (y & kInf) == kInf || ((y >> 16) & kInf) == kInf;
-          }
-        }
-        const uint32_t found = __ballot_sync(0xFFFFFFFFu, unfit && key >= f.ends);
-        if (lane == 0) ms.unfit[warp] = found;
-        named_bar_sync(2, kSoftmax);
-        const uint32_t all = ms.unfit[warp & 1] | ms.unfit[2 + (warp & 1)] | ms.unfit[4 + (warp & 1)] | ms.unfit[6 + (warp & 1)];
-        if ((all >> lane) & 1) {
-#pragma unroll 1
-          for (int x = 0; x < 16; ++x)
-            *reinterpret_cast<uint4*>(krow + (x >> 3) * kChunkBytes + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-          if (FP8 && warp < 2) ms.scale[b][2][key] = 0.f;
-        }
-        // a row that sees such a key gets NaN, also where its score is -inf (its weight 0, times a value that is gone)
-        const uint32_t lo = ms.unfit[0] | ms.unfit[2] | ms.unfit[4] | ms.unfit[6];
-        const uint32_t hi = ms.unfit[1] | ms.unfit[3] | ms.unfit[5] | ms.unfit[7];
-        const unsigned long long here = pack_u32x2(lo, hi) >> cq;
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          const int bit = 8 * (j >> 2) + (j & 1);
-          if (((here >> bit) & 1) && cq + bit < f.ends + trow[(j >> 1) & 1]) r[j] = 0x7FC00000u;
-        }
-      };
       // The weights of this thread's keys, with the reference maxima as they
       // are, and their sums (packed pairs of keys).
       auto weigh = [&]() {
@@ -1137,10 +1135,14 @@ __global__ void __launch_bounds__(Shape<FP8>::kThreads, 1) latent_attn_kernel(co
             half_max[wg * kAttnCols + rr] = mx[0];
             half_max[wg * kAttnCols + rr + 8] = mx[1];
           }
-          if (!PAGED) {
+          if (!PAGED || p.R == 1) {  // (one row a request: it sees every key that exists)
             named_bar_sync(2, kSoftmax);
           } else if (bar_red_or(2, kSoftmax, suspect)) {
-            drop_unfit_keys();
+            const int first = drop_unfit_keys<FP8>(ms, smem + kOffK + b * kStageBytes, b, (i >> 1) & 1, f.ends, abort_flag, limit);
+            // a row that sees such a key gives NaN, also where its score is -inf (a weight of 0, times a value that is gone)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (first < f.ends + trow[h]) l[h] = __uint_as_float(0x7FC00000u);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
