@@ -148,7 +148,7 @@ def set_wait_limit_ns(ns: int) -> None:
 
 
 def debug_withhold_first_tile(on: bool) -> None:
-    """Tests only: later fused / paged calls never load their first key tile,
+    """Tests only: later fused / paged / latent attention calls never load their first key tile,
     so a bounded wait runs out and the call reports WAIT_TIMEOUT."""
     lib().fp8idx_debug_withhold_first_tile(1 if on else 0)
 

@@ -38,14 +38,18 @@
 // weights take the place of the rotated part, which only the scores read.
 //
 // What bounds it: shared memory's 128 bytes a cycle.  A tile's score products
-// read 36 x 4 KB (measured: 33 cycles each), its value products 16 x 6 KB (49
-// cycles), its keys are written once, 72 KB: 2500 cycles.  4096 rows x 64
-// heads x 2048 bf16 keys take 1.46 ms (800 TFLOP/s), 2980 cycles a tile with
-// the segments' starts and ends; fp8 codes are written, read and written again
-// (another 64 KB) and take about 3800 (1024 rows x 128 heads: 0.94 ms).  Stages of 64 keys are the largest of which two fit beside
-// the queries; over one tile or two, waits for memory and hand-overs count:
-// one row of 16 heads x 2048 keys, a tile a CTA, takes 10.7 us.  Long
-// contexts with 64 columns a request reach 5.4 TB/s of keys.
+// read 36 x 4 KB (measured: 33 cycles each, which M = 64 on half of the tensor
+// core would take too), its value products 16 x 6 KB (49 cycles; the tensor
+// core alone would need 32), its keys are written once, 72 KB: 2500 cycles.
+// 4096 rows x 64 heads x 2048 bf16 keys take 1.46 ms (800 TFLOP/s) in a graph of
+// three calls and 1.60 ms (730) back to back, where the power limit lowers the
+// clock: 2980 cycles a tile with the segments' starts and ends.  fp8 codes are
+// written, read and written again (another 64 KB) and take about 3800 (1024
+// rows x 128 heads: 0.94 ms either way).  Stages of 64 keys are the largest of
+// which two fit beside the queries; over one tile or two, waits for memory and
+// hand-overs count: one row of 16 heads x 2048 keys, a tile a CTA, takes 10.6 us
+// in a graph, 10.9 a call.  Long contexts with 64 columns a request reach 5.5
+// TB/s of keys in a graph of three calls (0.91 ms), 4.6 back to back (1.09).
 #include <cstdint>
 
 #include "kernels.cuh"

@@ -60,10 +60,13 @@ constexpr int64_t kJoinTiles = 4, kJoinTilesWide = 6;
 // One CTA per SM, split into column blocks of 64 (a block of every range runs
 // at the same time as the others of that range, so that they share its keys
 // in L2) and as many ranges of the tile axis as fit; a range holds at least
-// one tile.  Where all groups have the same number of tiles (`uniform`), the
-// ranges end with groups if that makes the longest one at most kJoinTiles (or
-// kJoinTilesWide) longer: nothing is then left to be joined; or else, under the same
-// condition, every group gets ranges of its own.
+// min_tiles tiles (two for more than 32 columns, else one), where there are more
+// tiles than groups.  Where all groups have the same number of tiles (`uniform`):
+//  - the ranges end with groups, so that nothing is left to be joined, if that
+//    makes the longest one at most kJoinTiles tiles longer than an even share
+//    (kJoinTilesWide for more than 32 columns and fewer than two ranges a group);
+//  - or else, if there are no more groups than ranges, every group gets ranges of
+//    its own, if that makes the longest one at most kJoinTiles longer.
 AttnPlan plan_attn(int64_t groups, int64_t cols, int64_t tiles_per_group, bool uniform, int sms) {
   AttnPlan pl;
   pl.ncg = static_cast<int>(ceil_div(cols, kAttnCols));

@@ -377,7 +377,7 @@ int fp8idx_num_sms(void);
  * timeout path). */
 void fp8idx_set_wait_limit_ns(uint64_t ns);
 /* Tests only (no counterpart on the pages).  While `on` is nonzero, each CTA
- * of the fused and paged calls made afterwards never issues the load of its
+ * of the fused, paged and latent attention calls made afterwards never issues the load of its
  * first key tile, so the MMA's bounded wait on that tile runs out after the
  * wait limit: the call returns with FP8IDX_STATUS_WAIT_TIMEOUT set and its
  * outputs invalid, and the context stays usable.  Off by default. */
